@@ -1,6 +1,7 @@
 // Host side of the C ABI declared in include/moe.h: argument checks, the
 // workspace, and the kernel launches of each stage.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "moe_internal.cuh"
@@ -373,6 +374,108 @@ moe_status moe_layer_bufs(const moe_shape* shape, const void* x, const float* lo
   if ((st = do_dispatch(c, x, topk_idx, bufs)) != MOE_OK) return st;
   if ((st = do_ffn(c, bufs, w, y)) != MOE_OK) return st;
   return do_combine(c, bufs, y, topk_w, out);
+}
+
+// ---- gate ----------------------------------------------------------------------
+
+namespace moe {
+namespace {
+
+moe_status check_gate(const moe_shape* s, const moe_gate_desc* g) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (!g || (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID)) return MOE_ERR_INVALID_ARG;
+  if (!is_dtype(g->logits_dtype)) return MOE_ERR_INVALID_ARG;
+  if (g->logits_dtype == MOE_E4M3) return MOE_ERR_UNSUPPORTED;
+  if (g->groups < 1 || g->groups > 32 || s->E % g->groups != 0) return MOE_ERR_INVALID_ARG;
+  const int64_t n = s->E / g->groups;
+  if (g->topk_groups < 1 || g->topk_groups > g->groups || s->topk > g->topk_groups * n) return MOE_ERR_INVALID_ARG;
+  if (g->group_best < 1 || g->group_best > 2 || g->group_best > n || !std::isfinite(g->scale))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status current_sms(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+// Windows: both arrays with 1..1024 experts, or neither.
+bool windows_ok(int64_t experts, const int32_t* offsets, const int32_t* counts) {
+  return offsets && counts && experts >= 1 && experts <= 1024;
+}
+
+}  // namespace
+}  // namespace moe
+
+moe_status moe_gate(const moe_shape* shape, const moe_gate_desc* gate, const void* logits, const float* bias,
+                    int32_t* topk_idx, float* topk_w, void* ws, moe_stream_t stream) {
+  moe_status st = check_gate(shape, gate);
+  if (st != MOE_OK) return st;
+  if (shape->T > 0 && (!logits || !topk_idx || !topk_w)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(bias) || !aligned16(topk_idx) || !aligned16(topk_w)) return MOE_ERR_INVALID_ARG;
+  Ctx c;
+  if ((st = make_ctx(shape, ws, stream, &c)) != MOE_OK) return st;
+  if (shape->T == 0) return MOE_OK;
+  return cuda_status(launch_gate(c, *gate, logits, bias, topk_idx, topk_w));
+}
+
+moe_status moe_gate_backward(const moe_shape* shape, const moe_gate_desc* gate, const void* logits,
+                             const int32_t* topk_idx, const float* grad_w, void* grad_logits, moe_stream_t stream) {
+  moe_status st = check_gate(shape, gate);
+  if (st != MOE_OK) return st;
+  if (shape->T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !grad_w || !grad_logits) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(topk_idx) || !aligned16(grad_w) || !aligned16(grad_logits))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(
+      launch_gate_backward(*shape, *gate, logits, topk_idx, grad_w, grad_logits, (cudaStream_t)stream));
+}
+
+// ---- 8-bit integer products ----------------------------------------------------
+
+moe_status moe_quant_i8(int64_t rows, int64_t cols, int32_t src_dtype, const void* x, int64_t experts,
+                        const int32_t* offsets, const int32_t* counts, int8_t* q, float* scale,
+                        moe_stream_t stream) {
+  if (rows < 0 || rows > INT32_MAX || cols < 0 || cols > (1 << 24) || cols % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (!is_dtype(src_dtype)) return MOE_ERR_INVALID_ARG;
+  if (src_dtype == MOE_E4M3) return MOE_ERR_UNSUPPORTED;
+  const bool all = experts == 0 && !offsets && !counts;
+  if (!all && !windows_ok(experts, offsets, counts)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned16(scale)) return MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  moe_status st = current_sms(&sms);
+  if (st != MOE_OK) return st;
+  const RowWindows win{offsets, counts, all ? 1 : (int)experts};
+  return cuda_status(launch_quant_i8(rows, cols, src_dtype, x, win, q, scale, sms, (cudaStream_t)stream));
+}
+
+moe_status moe_gemm_i8(const moe_gemm_i8_desc* d, const int8_t* x, const float* x_scale, const int8_t* w,
+                       const float* w_scale, const int8_t* w_up, const float* up_scale, const int32_t* offsets,
+                       const int32_t* counts, void* y, void* ws, moe_stream_t stream) {
+  if (!d || d->reserved != 0 || d->M < 0 || d->M > INT32_MAX || d->N < 1 || d->K < 16 || d->K > 131056 ||
+      d->K % 16 != 0 || d->fill < 0 || d->experts < 1 || d->experts > 1024 || d->N > INT32_MAX / d->experts)
+    return MOE_ERR_INVALID_ARG;
+  if (!is_dtype(d->out_dtype)) return MOE_ERR_INVALID_ARG;
+  if (d->out_dtype == MOE_E4M3) return MOE_ERR_UNSUPPORTED;
+  const bool dense = d->experts == 1 && !offsets && !counts;
+  if (!dense && !windows_ok(d->experts, offsets, counts)) return MOE_ERR_INVALID_ARG;
+  if ((w_up == nullptr) != (up_scale == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!ws || ((uintptr_t)ws & 255u) != 0) return MOE_ERR_INVALID_ARG;
+  if (d->M == 0) return MOE_OK;
+  if (!x || !x_scale || !w || !w_scale || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(x_scale) || !aligned16(w) || !aligned16(w_scale) || !aligned16(w_up) ||
+      !aligned16(up_scale) || !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  GemmI8Args a{*d, x, x_scale, w, w_scale, w_up, up_scale, RowWindows{offsets, counts, (int)d->experts}, y,
+               (Header*)ws, 0, (cudaStream_t)stream};
+  moe_status st = current_sms(&a.num_sms);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_gemm_i8(a));
 }
 
 // ---- expert parallelism ------------------------------------------------------

@@ -341,6 +341,53 @@ bool ffn_tc_supported(const moe_shape& s);
 bool ffn_pair_supported(const Ctx& c);
 cudaError_t launch_ffn_pair(const Ctx& c, const moe_dispatch_bufs& b, const moe_weights& w, void* y);
 
+// the gate (gate.cu)
+cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits, const float* bias, int32_t* idx,
+                        float* w);
+cudaError_t launch_gate_backward(const moe_shape& s, const moe_gate_desc& g, const void* logits, const int32_t* idx,
+                                 const float* grad_w, void* grad_logits, cudaStream_t stream);
+
+// int8 products (quant_i8.cu, gemm_i8.cu): all rows (offsets == NULL) or the
+// filled rows of `experts` windows
+struct RowWindows {
+  const int32_t* offsets;
+  const int32_t* counts;
+  int experts;
+};
+
+// Rows of window e inside the M rows, first row in *row0 (0 rows for an
+// offset or a count out of range).
+__device__ __forceinline__ int window_rows(const RowWindows& w, int e, int64_t M, int64_t* row0) {
+  if (!w.offsets) {
+    *row0 = 0;
+    return (int)M;
+  }
+  const int64_t o = __ldg(w.offsets + e);
+  *row0 = o;
+  if (o < 0 || o >= M) return 0;
+  const int64_t n = __ldg(w.counts + e);
+  return n <= 0 ? 0 : (int)(n < M - o ? n : M - o);
+}
+
+cudaError_t launch_quant_i8(int64_t rows, int64_t cols, int32_t dtype, const void* x, const RowWindows& win,
+                            int8_t* q, float* scale, int num_sms, cudaStream_t stream);
+
+struct GemmI8Args {
+  moe_gemm_i8_desc d;
+  const int8_t* x;
+  const float* xs;
+  const int8_t* w;
+  const float* ws;
+  const int8_t* wu;    // NULL: no gate/up
+  const float* wus;
+  RowWindows win;
+  void* y;
+  Header* hdr;
+  int num_sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_gemm_i8(const GemmI8Args& a);
+
 // expert parallelism (ep.cu); g describes this rank, `all` the rank-major ranges
 cudaError_t launch_ep_count(const Ctx& c, const EpGeom& g, const int32_t* idx, const moe_ep_windows& all);
 cudaError_t launch_ep_layout(const Ctx& c, const EpGeom& g, const moe_ep_windows& all);

@@ -28,7 +28,8 @@ EXPORTS = ("moe_workspace_bytes", "moe_workspace_init", "moe_route", "moe_dispat
            "moe_grouped_ffn", "moe_combine", "moe_layer", "moe_layer_bufs", "moe_layer_workspace_bytes",
            "moe_poll_status", "moe_status_string", "moe_dispatch_noalloc", "moe_pack_mx_scales",
            "moe_layer_overlap", "moe_ep_sizes", "moe_ep_workspace_init", "moe_ep_count", "moe_ep_layout",
-           "moe_ep_dispatch", "moe_ep_grouped_ffn", "moe_ep_combine")
+           "moe_ep_dispatch", "moe_ep_grouped_ffn", "moe_ep_combine",
+           "moe_gate", "moe_gate_backward", "moe_quant_i8", "moe_gemm_i8")
 
 
 class MoeError(RuntimeError):
@@ -62,6 +63,20 @@ class moe_overlap(ctypes.Structure):
     _fields_ = [("dispatch_stream", ctypes.c_void_p), ("fork_event", ctypes.c_void_p),
                 ("join_event", ctypes.c_void_p), ("dispatch_sms", ctypes.c_int32),
                 ("ffn_sms", ctypes.c_int32)]
+
+
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+
+
+class moe_gate_desc(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("logits_dtype", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_best", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class moe_gemm_i8_desc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("experts", ctypes.c_int64), ("fill", ctypes.c_int64),
+                ("out_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 MOE_EP_SENTINEL, MOE_EP_FENCE = 0, 1
@@ -116,6 +131,10 @@ def lib() -> ctypes.CDLL:
             "moe_ep_grouped_ffn": [S, ctypes.POINTER(moe_ep), ctypes.POINTER(moe_weights),
                                    ctypes.POINTER(moe_ep_windows), P],
             "moe_ep_combine": [S, ctypes.POINTER(moe_ep), P, P, ctypes.POINTER(moe_ep_windows), P, P],
+            "moe_gate": [S, ctypes.POINTER(moe_gate_desc), P, P, P, P, P, P],
+            "moe_gate_backward": [S, ctypes.POINTER(moe_gate_desc), P, P, P, P, P],
+            "moe_quant_i8": [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, P, ctypes.c_int64, P, P, P, P, P],
+            "moe_gemm_i8": [ctypes.POINTER(moe_gemm_i8_desc), P, P, P, P, P, P, P, P, P, P, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -268,6 +287,105 @@ def moe_pack_mx_scales(src: torch.Tensor, stream=None) -> torch.Tensor:
     _check("moe_pack_mx_scales", lib().moe_pack_mx_scales(n, rows, groups * 32, _ptr(src), _ptr(dst),
                                                            _stream(stream)))
     return dst
+
+
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+
+
+def make_gate(score: str = "softmax", groups: int = 1, topk_groups: int = 1, group_best: int = 1,
+              scale: float = 1.0, logits: str = F32) -> moe_gate_desc:
+    """Description of a gate (moe_gate_desc); `logits` is the logits' dtype."""
+    return moe_gate_desc(_SCORES[score], _DT[logits], groups, topk_groups, group_best, scale)
+
+
+def _dense(fn: str, name: str, t, shape, *dtypes) -> None:
+    """A contiguous tensor on the current device of this shape and one of
+    these dtypes, as the library reads it; anything else raises."""
+    if (t is None or not t.is_cuda or t.get_device() != torch.cuda.current_device() or not t.is_contiguous()
+            or tuple(t.shape) != tuple(shape) or t.dtype not in dtypes):
+        got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}"
+        raise ValueError(f"{fn}: {name} must be a contiguous tensor on the current CUDA device, of shape "
+                         f"{tuple(shape)} and dtype {' or '.join(str(d) for d in dtypes)}, got {got}")
+
+
+def _gate_args(fn, shape, gate, logits, topk_idx, w) -> None:
+    ks = shape.topk + (shape.flags & 1)
+    dt = torch.bfloat16 if gate.logits_dtype == MOE_BF16 else torch.float32
+    _dense(fn, "logits", logits, (shape.T, shape.E), dt)
+    _dense(fn, "topk_idx", topk_idx, (shape.T, ks), torch.int32)
+    _dense(fn, "topk weights", w, (shape.T, ks), torch.float32)
+
+
+def moe_gate(shape, gate: moe_gate_desc, logits, bias, topk_idx, topk_w, ws, stream=None) -> None:
+    """Routing by scores, an optional balance bias [E] and expert groups
+    (moe_gate in include/moe.h); outputs as moe_route's."""
+    _gate_args("moe_gate", shape, gate, logits, topk_idx, topk_w)
+    if bias is not None:
+        _dense("moe_gate", "bias", bias, (shape.E,), torch.float32)
+    _check("moe_gate", lib().moe_gate(ctypes.byref(shape), ctypes.byref(gate), _ptr(logits), _ptr(bias),
+                                      _ptr(topk_idx), _ptr(topk_w), _ptr(ws), _stream(stream)))
+
+
+def moe_gate_backward(shape, gate: moe_gate_desc, logits, topk_idx, grad_w, grad_logits, stream=None) -> None:
+    """grad_logits [T, E] from the gradient of moe_gate's weights."""
+    _gate_args("moe_gate_backward", shape, gate, logits, topk_idx, grad_w)
+    _dense("moe_gate_backward", "grad_logits", grad_logits, logits.shape, logits.dtype)
+    _check("moe_gate_backward", lib().moe_gate_backward(ctypes.byref(shape), ctypes.byref(gate), _ptr(logits),
+                                                        _ptr(topk_idx), _ptr(grad_w), _ptr(grad_logits),
+                                                        _stream(stream)))
+
+
+_SRC = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _windows(fn, offsets, counts) -> int:
+    """Number of windows (0: all rows)."""
+    if offsets is None and counts is None:
+        return 0
+    n = 0 if offsets is None else offsets.numel()
+    _dense(fn, "offsets", offsets, (n,), torch.int32)
+    _dense(fn, "counts", counts, (n,), torch.int32)
+    return n
+
+
+def moe_quant_i8(x, q, scale, offsets=None, counts=None, stream=None) -> None:
+    """Rows of x [rows, cols] (f32 or bf16) to int8 q [rows, cols] with one
+    scale [rows] each; with windows (offsets, counts) only their filled rows."""
+    fn = "moe_quant_i8"
+    if x.dim() != 2:
+        raise ValueError(f"{fn}: x must be [rows, cols], got {tuple(x.shape)}")
+    _dense(fn, "x", x, x.shape, torch.float32, torch.bfloat16)
+    _dense(fn, "q", q, x.shape, torch.int8)
+    _dense(fn, "scale", scale, x.shape[:1], torch.float32)
+    n = _windows(fn, offsets, counts)
+    _check(fn, lib().moe_quant_i8(x.shape[0], x.shape[1], _SRC[x.dtype], _ptr(x), n, _ptr(offsets), _ptr(counts),
+                                  _ptr(q), _ptr(scale), _stream(stream)))
+
+
+def moe_gemm_i8(x, x_scale, w, w_scale, y, ws, w_up=None, up_scale=None, offsets=None, counts=None,
+                fill: int = 0, stream=None) -> None:
+    """y [M, N] (bf16 or f32) from int8 rows x [M, K] with scales [M] and int8
+    weights w [N, K] with scales [N], or, over windows, w [E, N, K] and
+    [E, N]; with w_up and up_scale, silu(x w^T) * (x w_up^T). `fill` rows are
+    expected to be filled over all windows (0: all; chooses tiles only)."""
+    fn = "moe_gemm_i8"
+    if x.dim() != 2 or w.dim() not in (2, 3):
+        raise ValueError(f"{fn}: x must be [M, K] and w [N, K] or [E, N, K], got {tuple(x.shape)}, {tuple(w.shape)}")
+    n = _windows(fn, offsets, counts)
+    E = w.shape[0] if w.dim() == 3 else 1
+    if n and n != E:
+        raise ValueError(f"{fn}: {n} windows for the weights of {E} experts")
+    d = moe_gemm_i8_desc(x.shape[0], w.shape[-2], x.shape[1], E, fill, _SRC.get(y.dtype, -1), 0)
+    _dense(fn, "x", x, x.shape, torch.int8)
+    _dense(fn, "x_scale", x_scale, (d.M,), torch.float32)
+    _dense(fn, "w", w, w.shape[:-1] + (d.K,), torch.int8)
+    _dense(fn, "w_scale", w_scale, w.shape[:-1], torch.float32)
+    if w_up is not None or up_scale is not None:
+        _dense(fn, "w_up", w_up, w.shape, torch.int8)
+        _dense(fn, "up_scale", up_scale, w_scale.shape, torch.float32)
+    _dense(fn, "y", y, (d.M, d.N), torch.bfloat16, torch.float32)
+    _check(fn, lib().moe_gemm_i8(ctypes.byref(d), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(w_up),
+                                 _ptr(up_scale), _ptr(offsets), _ptr(counts), _ptr(y), _ptr(ws), _stream(stream)))
 
 
 def moe_dispatch_noalloc(shape, x, topk_idx, bufs: moe_dispatch_bufs, stream=None) -> None:

@@ -11,9 +11,11 @@
  *   moe_combine      top-k weighted gather-reduce back to token order
  *
  * and moe_layer, which enqueues all four; moe_layer_overlap, the same layer with
- * dispatch running beside the grouped FFN on a partition of the SMs; and the
+ * dispatch running beside the grouped FFN on a partition of the SMs; the
  * expert-parallel calls moe_ep_* (experts split over ranks, tokens pushed into
- * the owners' rank-major windows). The stage split follows the pages:
+ * the owners' rank-major windows); moe_gate and moe_gate_backward, routing by
+ * scores, a bias and expert groups with its gradient; and moe_quant_i8 and
+ * moe_gemm_i8, int8 products over the windows or dense. The stage split follows the pages:
  * an MoE layer is token dispatch, grouped GEMMs and a combine (GC-MoE feed
  * item, "Key points"; GC-MoE explainer, "Why Expert Parallelism Is
  * Inefficient in MoE Decoding"); dispatch pushes tokens into per-expert
@@ -412,6 +414,140 @@ MOE_API moe_status moe_dispatch_noalloc(const moe_shape* shape, const void* x, c
  */
 MOE_API moe_status moe_pack_mx_scales(int64_t n, int64_t rows, int64_t cols, const void* src, void* dst,
                                       moe_stream_t stream);
+
+/* ---- gate: routing with scores, a bias and expert groups, and its gradient ------
+ *
+ * moe_route chooses and weighs by a softmax of the logits. moe_gate covers the
+ * other routers of MoE layers (the pages leave the gating rule open):
+ *
+ *   s_e = softmax(l)_e, or sigmoid(l_e) = 1 / (1 + exp(-l_e))
+ *   c_e = s_e + bias_e, which only chooses (a bias that balances the experts'
+ *         load); without a bias the choice is made on the logits themselves,
+ *         which order as the scores do
+ *   groups > 1: experts e E/groups .. (e + 1) E/groups - 1 form a group, ranked
+ *         by the sum of its group_best largest c (of its largest s, where there
+ *         is no bias and group_best is 2); only the topk_groups best groups are
+ *         open
+ *   the topk largest c of the open experts, in descending order; the lower
+ *         index wins a tie, among groups too
+ *   w_j = scale * s_{e_j}, with shape->renorm = 1 divided by the sum of the
+ *         chosen scores
+ *
+ * The choice is that of the formulas in binary64: where two candidates come
+ * closer than binary32 can tell, they are compared again in binary64. Weights
+ * are binary32; renormalised ones keep their precision where all chosen
+ * scores underflow.
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+typedef struct moe_gate_desc {
+  int32_t score;         /* MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID */
+  int32_t logits_dtype;  /* MOE_F32 or MOE_BF16 (gradients too) */
+  int32_t groups;        /* 1..32, dividing E */
+  int32_t topk_groups;   /* 1..groups, with topk <= topk_groups * E / groups */
+  int32_t group_best;    /* 1 or 2, <= E / groups */
+  float scale;           /* finite */
+} moe_gate_desc;
+
+/*
+ * Routing by `gate`, an alternative to moe_route with the same outputs.
+ *   shape    the layer (T, E, topk, renorm and MOE_FLAG_SHARED_EXPERT are used:
+ *            with a shared expert the last slot is E with weight 1)
+ *   logits   [T, E] gate->logits_dtype, device
+ *   bias     [E] fp32, device, or NULL
+ *   topk_idx [T, topk] int32, device (out)
+ *   topk_w   [T, topk] fp32, device (out)
+ *   ws       workspace (error word)
+ * A token with a non-finite logit (or a non-finite bias) latches
+ * MOE_ERR_NONFINITE and gets experts 0 .. topk - 1 with weight NaN.
+ */
+MOE_API moe_status moe_gate(const moe_shape* shape, const moe_gate_desc* gate, const void* logits,
+                            const float* bias, int32_t* topk_idx, float* topk_w, void* ws,
+                            moe_stream_t stream);
+
+/*
+ * Gradient of moe_gate's weights with respect to the logits, for the choice
+ * given (which has no gradient itself, so the bias has none):
+ *   grad_logits[t, e] = sum_j grad_w[t, j] * d w_j / d l_e
+ *   logits      [T, E] gate->logits_dtype, device: moe_gate's input
+ *   topk_idx    [T, topk] int32, device: moe_gate's choice. A slot outside
+ *               [0, E) takes no part, as if it had not been chosen; an expert
+ *               named twice counts twice (in the sum of renormalised weights too)
+ *   grad_w      [T, topk] fp32, device
+ *   grad_logits [T, E] gate->logits_dtype, device (out, every element written)
+ * With a shared expert topk_idx and grad_w have topk + 1 columns, the last
+ * without effect. The order of sums is fixed. Non-finite logits give NaN.
+ */
+MOE_API moe_status moe_gate_backward(const moe_shape* shape, const moe_gate_desc* gate, const void* logits,
+                                     const int32_t* topk_idx, const float* grad_w, void* grad_logits,
+                                     moe_stream_t stream);
+
+/* ---- 8-bit integer products ----------------------------------------------------
+ *
+ * Linear layers and experts with int8 weights (one scale per output channel)
+ * on int8 rows (one scale per token), the W8A8 form of a checkpoint. Rows can
+ * be all of a matrix, or only the filled rows of `experts` windows: window e
+ * is rows offsets[e] .. offsets[e] + counts[e] - 1, as moe_dispatch lays them
+ * out (moe_dispatch_bufs). Windows must not overlap; what a window holds
+ * past the last of the M rows (or of a negative offset) is not worked on.
+ * Other rows are neither read into a result nor written. These are serving
+ * calls: integers have no gradient.
+ *
+ * With the stages above, an int8 layer is: moe_route or moe_gate, moe_dispatch
+ * of a bf16 layer, moe_quant_i8 of xq, moe_gemm_i8 with gate and up weights,
+ * moe_quant_i8 of its output, moe_gemm_i8 with the down weights, moe_combine.
+ */
+
+/*
+ * Rows to int8 with one scale each:
+ *   scale[r] = max_k |x[r, k]| / 127 (at least 2^-126; 1 for a row of zeros)
+ *   q[r, k]  = x[r, k] / scale[r], rounded to nearest, ties to even
+ * both divisions correctly rounded in binary32, so q is the same everywhere.
+ *   rows, cols  >= 0; cols a multiple of 16, at most 2^24
+ *   src_dtype   MOE_F32 or MOE_BF16
+ *   x           [rows, cols] src_dtype, device
+ *   experts, offsets, counts  windows ([experts] int32, device), or 0, NULL, NULL
+ *               for all rows; experts <= 1024
+ *   q           [rows, cols] int8, device (out), -127 .. 127
+ *   scale       [rows] fp32, device (out)
+ * A row with a NaN or an infinity gets scale NaN and q = 0, so that what is
+ * computed from it is NaN. q and scale must not overlap x.
+ */
+MOE_API moe_status moe_quant_i8(int64_t rows, int64_t cols, int32_t src_dtype, const void* x, int64_t experts,
+                                const int32_t* offsets, const int32_t* counts, int8_t* q, float* scale,
+                                moe_stream_t stream);
+
+typedef struct moe_gemm_i8_desc {
+  int64_t M;         /* rows of x and y, 0 .. 2^31 - 1 */
+  int64_t N;         /* output channels of one expert, >= 1; experts * N < 2^31 */
+  int64_t K;         /* a multiple of 16, 16 .. 131056: the sums stay below 2^31 */
+  int64_t experts;   /* 1..1024; windows need offsets and counts, 1 without them is a dense product */
+  int64_t fill;      /* rows expected to be filled over all windows, 0 = M: chooses the
+                        kernel's tiles, never the result */
+  int32_t out_dtype; /* MOE_BF16 or MOE_F32 */
+  int32_t reserved;  /* 0 */
+} moe_gemm_i8_desc;
+
+/*
+ * Product with int8 rows and weights, exact in int32, then scaled in fp32 and
+ * rounded once to out_dtype: for every row r of window e and channel n
+ *   p(w, ws)[r, n] = (sum_k x[r, k] * w[e, n, k]) * ws[e, n] * x_scale[r]
+ *   y[r, n] = p(w, w_scale), or with w_up
+ *   y[r, n] = silu(p(w, w_scale)) * p(w_up, up_scale)
+ *   x        [M, K] int8, device
+ *   x_scale  [M] fp32, device
+ *   w, w_up  [experts, N, K] int8, device, read only; w_up may be NULL
+ *   w_scale, up_scale  [experts, N] fp32, device; up_scale with w_up only
+ *   offsets, counts    [experts] int32, device, or both NULL (experts = 1)
+ *   y        [M, N] out_dtype, device (out); rows of no window are left as they
+ *            were. y must not overlap the inputs
+ *   ws       workspace (error word; any prepared workspace serves): a wait that
+ *            runs out latches MOE_ERR_TIMEOUT
+ */
+MOE_API moe_status moe_gemm_i8(const moe_gemm_i8_desc* desc, const int8_t* x, const float* x_scale,
+                               const int8_t* w, const float* w_scale, const int8_t* w_up, const float* up_scale,
+                               const int32_t* offsets, const int32_t* counts, void* y, void* ws,
+                               moe_stream_t stream);
 
 /* ---- expert parallelism ------------------------------------------------------
  *
