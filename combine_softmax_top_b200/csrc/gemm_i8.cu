@@ -1,85 +1,457 @@
-// int8 products over dense rows or expert windows: exact int32 sums, scaled in
-// fp32 and rounded once.
+// int8 products over dense rows or expert windows on the 5th-generation
+// tensor cores (tcgen05 kind::i8): exact int32 sums, scaled in fp32 and rounded
+// once, y[r, n] = (sum_k x[r, k] w[n, k]) ws[n] xs[r], or silu(gate) * up of two
+// such products.
 //
-// One block computes tiles of 64 rows x 64 channels with the four-way integer
-// dot product; each of its 256 threads holds 4 x 4 sums (twice with an up
-// projection).
-#include "moe_internal.cuh"
+// The weights are the MMA's A operand (M = 128 channels a CTA) and the rows its
+// N operand, so a few rows cost few columns. A unit of work is (expert, channel
+// tile, chunk of up to kRows rows); a persistent grid takes the units in a
+// fixed order, which every warp derives by itself from the windows. With an up
+// projection a CTA's 128 A rows are 64 gate and 64 up channels, and the
+// epilogue brings the two halves of tensor memory together through shared
+// memory: the main loop is the same as without.
+//
+// Per CTA (320 threads): warp 0 streams K slabs of 128 bytes into a ring of
+// stages with TMA, warp 1 issues the MMAs into one of two accumulators, warps
+// 2-9 read the other one back, scale and store. Two forms:
+//   kG = 1  chunks of 64 rows, one CTA: a decode batch reads every weight once,
+//           and the many small stages keep the loads in flight that HBM needs
+//   kG = 2  chunks of 256 rows, a CTA pair (M = 256 over two SMs, each holding
+//           half of the rows): for many rows an expert, where the tensor cores
+//           and the L2's delivery of operands bound it
+// Every wait is bounded: on expiry the kernel latches MOE_ERR_TIMEOUT, drains
+// its copies and MMAs, frees tensor memory and exits.
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include "ffn_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 64, kThreads = 256, kWords = 16;   // K step: 16 words of 4 bytes
+using ffn::kABytes;
+using ffn::kMaxDynSmem;
+using ffn::kSlab;
+using ffn::wait_bar;
 
-template <bool kUp, typename O>
-__global__ void __launch_bounds__(kThreads) gemm_i8_kernel(GemmI8Args a) {
-  __shared__ int sx[kTile][kWords + 1], sw[kTile][kWords + 1], su[kTile][kWords + 1];
-  const int e = blockIdx.z, n0 = blockIdx.x * kTile;
-  const int64_t N = a.d.N, K = a.d.K;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int64_t row0;
-  const int rows = window_rows(a.win, e, a.d.M, &row0);
-  for (int64_t m0 = (int64_t)blockIdx.y * kTile; m0 < rows; m0 += (int64_t)gridDim.y * kTile) {
-    int acc[4][4] = {}, up[4][4] = {};
-    for (int64_t k0 = 0; k0 < K; k0 += 4 * kWords) {
-      // each thread moves one 16-byte piece of each tile (K is a multiple of 16)
-      const int r = threadIdx.x >> 2, p = threadIdx.x & 3;
-      const int64_t k = k0 + 16 * p;
-      int4 vx = make_int4(0, 0, 0, 0), vw = vx, vu = vx;
-      if (k < K) {
-        if (m0 + r < rows) vx = *reinterpret_cast<const int4*>(a.x + (row0 + m0 + r) * K + k);
-        if (n0 + r < N) {
-          vw = *reinterpret_cast<const int4*>(a.w + ((int64_t)e * N + n0 + r) * K + k);
-          if (kUp) vu = *reinterpret_cast<const int4*>(a.wu + ((int64_t)e * N + n0 + r) * K + k);
+constexpr int kThreads = 320;      // warps: 0 TMA, 1 MMA, 2-9 epilogue (two sets of four)
+constexpr int kEpiThreads = 256;
+constexpr int kMaxExperts = 1024;
+constexpr int kBand = 8;           // chunks that share each channel tile in turn (unit order)
+
+template <int kG, bool kUp>
+struct Form {
+  static constexpr int kRows = kG == 2 ? 256 : 64;            // rows of a chunk: MMA columns
+  static constexpr int kBRows = kRows / kG;                   // of them in this CTA's shared memory
+  static constexpr int kCh = kUp ? 64 : 128;                  // channels a CTA
+  static constexpr int kStage = kABytes + kBRows * kSlab;
+  static constexpr int kXchg = kUp ? 2 * 2 * 16 * 64 * 4 : 0; // [set][gate, up][16 rows][64 channels] int32
+  static constexpr int kXs = 2 * kRows * 4;                   // row scales, two units
+  static constexpr int kTab = (kMaxExperts + 1) * 4 + 12;
+  static constexpr int kCtl = 512;
+  static constexpr int kStages = (kMaxDynSmem - 1024 - kXchg - kXs - kTab - kCtl) / kStage;
+  static constexpr int kOffXchg = kStages * kStage;
+  static constexpr int kOffXs = kOffXchg + kXchg;
+  static constexpr int kOffTab = kOffXs + kXs;
+  static constexpr int kOffCtl = (kOffTab + kTab + 15) / 16 * 16;
+  static constexpr int kSmem = kOffCtl + kCtl + 1024;         // and alignment slack
+  static constexpr uint32_t kTmemCols = 2 * kRows;
+  static_assert(kSmem <= kMaxDynSmem && (2 * kStages + 5) * 8 <= kCtl - 32, "shared memory");
+};
+
+struct Params {
+  CUtensorMap tm_w, tm_wu;   // [experts * N, K], boxes of 128 (64 with up) channels
+  CUtensorMap tm_x, tm_x16;  // [M, K], boxes of kBRows and 16 rows
+  const float* xs;
+  const float* ws;
+  const float* wus;
+  RowWindows win;
+  void* y;
+  Header* hdr;
+  int64_t M, N;
+  int nk;        // K slabs
+  int tiles;     // channel tiles of one expert
+};
+
+// One unit: chunk `chunk` of expert e's rows, channel tile `tile`.
+struct Unit {
+  int e, tile, rows;
+  int64_t row;   // first row
+};
+
+template <int kG, bool kUp, typename O>
+__global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_constant__ Params p) {
+  using F = Form<kG, kUp>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* ctl = smem + F::kOffCtl;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ctl);      // [kStages] CTA 0: all halves landed
+  uint64_t* empty = full + F::kStages;                    // [kStages] each CTA: the stage's MMAs are done
+  uint64_t* acc_full = empty + F::kStages;                // [2] each CTA: an accumulator is complete
+  uint64_t* acc_empty = acc_full + 2;                     // [2] CTA 0: all epilogue warps have read it
+  uint64_t* drain = acc_empty + 2;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + F::kCtl - 32);
+  volatile int* epi_ok = abort_flag + 1;                  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctl + F::kCtl - 16);
+  int* tab = reinterpret_cast<int*>(smem + F::kOffTab);   // [experts + 1] first chunk of each expert
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = kG == 2 ? ptx::cluster_ctarank() : 0u;
+  const int worker = blockIdx.x / kG, workers = gridDim.x / kG;
+  const int E = p.win.experts;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < F::kStages; ++s) {
+      ptx::mbar_init(full + s, 1);
+      ptx::mbar_init(empty + s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(acc_full + s, 1);
+      ptx::mbar_init(acc_empty + s, 8 * kG);
+    }
+    ptx::mbar_init(drain, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    if constexpr (kG == 2) {
+      ptx::tmem_alloc_pair(tmem_slot, F::kTmemCols);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(tmem_slot, F::kTmemCols);
+      ptx::tmem_relinquish();
+    }
+  }
+  if (warp == 2) {   // first chunk of every expert
+    int first = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      int64_t row0;
+      const int n = e0 + lane < E ? (window_rows(p.win, e0 + lane, p.M, &row0) + F::kRows - 1) / F::kRows : 0;
+      int inc = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += v;
+      }
+      if (e0 + lane < E) tab[e0 + lane] = first + inc - n;
+      first += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) tab[E] = first;
+  }
+  ptx::tc_fence_before();
+  if constexpr (kG == 2) ptx::cluster_sync();   // both CTAs' barriers and tensor memory exist
+  else __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t units = (int64_t)tab[E] * p.tiles;
+
+  auto remote = [&](const void* q, uint32_t r) { return ptx::mapa_shared(ptx::smem_u32(q), r); };
+
+  // Unit u. Within an expert: bands of kBand chunks, in a band channel tile by
+  // channel tile, so that the workers of one moment share few rows and few
+  // channels in L2.
+  auto unit = [&](int64_t u) -> Unit {
+    const int64_t nt = p.tiles;
+    int lo = 0, hi = E - 1;   // the last expert whose first unit is <= u (empty ones never are)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tab[mid] * nt <= u) lo = mid;
+      else hi = mid - 1;
+    }
+    const int nc = tab[lo + 1] - tab[lo];
+    const int64_t v = u - tab[lo] * nt;
+    const int64_t band = v / (kBand * nt), w = v - band * kBand * nt;
+    const int left = nc - (int)band * kBand;
+    const int bh = left < kBand ? left : kBand;
+    const int chunk = (int)band * kBand + (int)(w % bh);
+    Unit r;
+    r.e = lo;
+    r.tile = (int)(w / bh);
+    int64_t row0;
+    const int rows = window_rows(p.win, lo, p.M, &row0) - chunk * F::kRows;
+    r.rows = rows < F::kRows ? rows : F::kRows;
+    r.row = row0 + (int64_t)chunk * F::kRows;
+    return r;
+  };
+  auto columns = [](int rows) { return (rows + 16 * kG - 1) / (16 * kG) * (16 * kG); };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer (both CTAs)
+    if (lane == 0) {
+      ptx::prefetch_tmap(&p.tm_w);
+      ptx::prefetch_tmap(&p.tm_x);
+      ptx::prefetch_tmap(&p.tm_x16);
+      if (kUp) ptx::prefetch_tmap(&p.tm_wu);
+    }
+    uint32_t stage = 0, phase = 0;
+    uint32_t armed = 0, armed_parity = 0;
+    const uint64_t pol = kG == 2 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
+    bool ok = true;
+    for (int64_t u = worker; ok && u < units; u += workers) {
+      const Unit j = unit(u);
+      const int n = columns(j.rows) / kG;                       // rows this CTA loads
+      const int wrow = (int)(j.e * p.N + (int64_t)j.tile * (kG * F::kCh) + rank * F::kCh);
+      const int xrow = (int)(j.row + rank * n);
+      for (int k = 0; k < p.nk; ++k) {
+        int good = 1;
+        if (lane == 0) good = wait_bar(empty + stage, phase ^ 1u, abort_flag, p.hdr, 0x48000000u | stage);
+        if (!__shfl_sync(0xffffffffu, good, 0)) { ok = false; break; }
+        __syncwarp();
+        uint8_t* st = smem + stage * F::kStage;
+        if (ptx::elect_one()) {
+          if (rank == 0) ptx::mbar_arrive_expect_tx(full + stage, (uint32_t)(kG * (kABytes + n * kSlab)));
+          const int kx = k * kSlab;
+          if constexpr (kG == 2) {
+            const uint32_t fb = remote(full + stage, 0);
+            ptx::tma_load_2d_pair(st, &p.tm_w, fb, kx, wrow);
+            if (kUp) ptx::tma_load_2d_pair(st + 64 * kSlab, &p.tm_wu, fb, kx, wrow);
+            if (n == F::kBRows) {
+              ptx::tma_load_2d_pair(st + kABytes, &p.tm_x, fb, kx, xrow);
+            } else {
+              for (int r = 0; r < n; r += 16)
+                ptx::tma_load_2d_pair(st + kABytes + r * kSlab, &p.tm_x16, fb, kx, xrow + r);
+            }
+          } else {
+            uint64_t* fb = full + stage;
+            ptx::tma_load_2d_hint(st, &p.tm_w, fb, kx, wrow, pol);
+            if (kUp) ptx::tma_load_2d_hint(st + 64 * kSlab, &p.tm_wu, fb, kx, wrow, pol);
+            if (n == F::kBRows) {
+              ptx::tma_load_2d(st + kABytes, &p.tm_x, fb, kx, xrow);
+            } else {
+              for (int r = 0; r < n; r += 16) ptx::tma_load_2d(st + kABytes + r * kSlab, &p.tm_x16, fb, kx, xrow + r);
+            }
+          }
+        }
+        __syncwarp();
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == (uint32_t)F::kStages) { stage = 0; phase ^= 1u; }
+      }
+    }
+    // drain (CTA 0): every load counted on its barriers has landed
+    if (rank == 0 && lane == 0) {
+      for (int s = 0; s < F::kStages; ++s) {
+        if (!((armed >> s) & 1u)) continue;
+        const unsigned long long t0 = globaltimer();
+        while (!ptx::mbar_try_wait(full + s, (armed_parity >> s) & 1u))
+          if (globaltimer() - t0 > kWaitBudgetNs) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer (CTA 0)
+    if (rank == 0) {
+      uint32_t stage = 0, phase = 0, i = 0;
+      bool ok = true;
+      for (int64_t u = worker; ok && u < units; u += workers, ++i) {
+        const uint32_t slot = i & 1u, use = (i >> 1) & 1u;
+        int good = 1;
+        if (lane == 0) good = wait_bar<kG == 2>(acc_empty + slot, use ^ 1u, abort_flag, p.hdr, 0x58000000u | slot);
+        if (!__shfl_sync(0xffffffffu, good, 0)) break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + slot * F::kRows;
+        const uint32_t idesc = ptx::idesc_i8(128 * kG, columns(unit(u).rows));
+        for (int k = 0; k < p.nk; ++k) {
+          if (lane == 0) good = wait_bar(full + stage, phase, abort_flag, p.hdr, 0x68000000u | stage);
+          if (!__shfl_sync(0xffffffffu, good, 0)) { ok = false; break; }
+          ptx::tc_fence_after();
+          uint8_t* st = smem + stage * F::kStage;
+          const uint64_t a = ptx::desc_kmajor_sw128(st), b = ptx::desc_kmajor_sw128(st + kABytes);
+          if (ptx::elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {   // 32 bytes of K per MMA
+              if constexpr (kG == 2) ptx::mma_i8_pair(d, a + 2 * kk, b + 2 * kk, idesc, (k | kk) ? 1u : 0u);
+              else ptx::mma_i8(d, a + 2 * kk, b + 2 * kk, idesc, (k | kk) ? 1u : 0u);
+            }
+            if constexpr (kG == 2) {
+              ptx::mma_commit_pair(remote(empty + stage, 0));
+              ptx::mma_commit_pair(remote(empty + stage, 1));
+            } else {
+              ptx::mma_commit(empty + stage);
+            }
+          }
+          __syncwarp();
+          if (++stage == (uint32_t)F::kStages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        if (ptx::elect_one()) {
+          if constexpr (kG == 2) {
+            ptx::mma_commit_pair(remote(acc_full + slot, 0));
+            ptx::mma_commit_pair(remote(acc_full + slot, 1));
+          } else {
+            ptx::mma_commit(acc_full + slot);
+          }
+        }
+        __syncwarp();
+      }
+      if (ptx::elect_one()) {   // every MMA issued is complete
+        if constexpr (kG == 2) ptx::mma_commit_pair(remote(drain, 0));
+        else ptx::mma_commit(drain);
+        const unsigned long long t0 = globaltimer();
+        while (!ptx::mbar_try_wait(drain, 0))
+          if (globaltimer() - t0 > kWaitBudgetNs) break;
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    // Warp w reads tensor-memory lanes 32 (w % 4) .. + 31 (A rows); set s takes
+    // the 32-column batches s, s + 2, ...
+    const int q = warp & 3, et = threadIdx.x - 64, set = et >> 7;
+    const int arow = q * 32 + lane;
+    const int ch = kUp ? arow & 63 : arow;           // channel of the CTA's tile
+    int* xg = reinterpret_cast<int*>(smem + F::kOffXchg) + set * 2 * 16 * 64;   // [16][64]
+    int* xu = xg + 16 * 64;
+    float* xs_all = reinterpret_cast<float*>(smem + F::kOffXs);
+    uint32_t i = 0;
+    for (int64_t u = worker; u < units; u += workers, ++i) {
+      const Unit j = unit(u);
+      const uint32_t slot = i & 1u, use = (i >> 1) & 1u;
+      float* xs = xs_all + slot * F::kRows;
+      const int64_t n0 = (int64_t)j.tile * (kG * F::kCh) + rank * F::kCh + ch;
+      const bool real = n0 < p.N;
+      const float sw = real ? __ldg(p.ws + j.e * p.N + n0) : 0.f;
+      const float su = kUp && real ? __ldg(p.wus + j.e * p.N + n0) : 0.f;
+      if (et < j.rows) xs[et] = __ldg(p.xs + j.row + et);
+      // one thread waits and tells the others, so that all leave together
+      if (et == 0) epi_ok[slot] = wait_bar(acc_full + slot, use, abort_flag, p.hdr, 0x78000000u | slot);
+      ptx::named_barrier(1, kEpiThreads);
+      if (!epi_ok[slot]) break;
+      while (!ptx::mbar_try_wait(acc_full + slot, use)) {}   // completed: returns at once
+      ptx::tc_fence_after();
+      const uint32_t d = tmem + slot * F::kRows + ((uint32_t)(q * 32) << 16);
+      O* y = reinterpret_cast<O*>(p.y) + j.row * p.N + n0;
+      auto store = [&](int c, float v) {
+        if (c < j.rows && real) {
+          if constexpr (sizeof(O) == 2) y[(int64_t)c * p.N] = __float2bfloat16_rn(v);
+          else y[(int64_t)c * p.N] = v;
+        }
+      };
+      for (int c0 = 32 * set; c0 < j.rows; c0 += 64) {
+        uint32_t v[32];
+        ptx::tmem_ld_x32(d + c0, v);
+        ptx::tmem_wait_ld();
+        if constexpr (!kUp) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (c0 + c < j.rows) store(c0 + c, (float)(int)v[c] * sw * xs[c0 + c]);
+          }
+        } else {
+          // gate warps finish the batch's first 16 columns, up warps the last
+          const bool gate = q < 2;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            if (gate) xg[c * 64 + ch] = (int)v[16 + c];
+            else xu[c * 64 + ch] = (int)v[c];
+          }
+          ptx::named_barrier(2 + set, 128);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int col = c0 + (gate ? c : 16 + c);
+            if (col < j.rows) {
+              const int gi = gate ? (int)v[c] : xg[c * 64 + ch], ui = gate ? xu[c * 64 + ch] : (int)v[16 + c];
+              const float s = xs[col], g = (float)gi * sw * s;
+              store(col, g / (1.f + expf(-g)) * ((float)ui * su * s));
+            }
+          }
+          ptx::named_barrier(2 + set, 128);
         }
       }
-      __syncthreads();
-      const int* px = &vx.x;
-      const int* pw = &vw.x;
-      const int* pu = &vu.x;
-      for (int i = 0; i < 4; ++i) {
-        sx[r][4 * p + i] = px[i];
-        sw[r][4 * p + i] = pw[i];
-        if (kUp) su[r][4 * p + i] = pu[i];
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) ptx::mbar_arrive(acc_empty + slot);
+        else ptx::mbar_arrive_remote(remote(acc_empty + slot, 0));
       }
-      __syncthreads();
-      for (int kk = 0; kk < kWords; ++kk)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[i][j] = __dp4a(sx[ty + 16 * i][kk], sw[tx + 16 * j][kk], acc[i][j]);
-            if (kUp) up[i][j] = __dp4a(sx[ty + 16 * i][kk], su[tx + 16 * j][kk], up[i][j]);
-          }
     }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-        if (m >= rows || n >= N) continue;
-        const float xs = a.xs[row0 + m];
-        float v = (float)acc[i][j] * a.ws[(int64_t)e * N + n] * xs;
-        if (kUp) v = v / (1.f + expf(-v)) * ((float)up[i][j] * a.wus[(int64_t)e * N + n] * xs);
-        O* y = (O*)a.y + (row0 + m) * N + n;
-        if constexpr (sizeof(O) == 2) *y = __float2bfloat16_rn(v);
-        else *y = v;
-      }
   }
+  // every role is done in both CTAs before tensor memory is freed
+  ptx::tc_fence_before();
+  if constexpr (kG == 2) ptx::cluster_sync();
+  else __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    if constexpr (kG == 2) ptx::tmem_dealloc_pair(tmem, F::kTmemCols);
+    else ptx::tmem_dealloc(tmem, F::kTmemCols);
+  }
+}
+
+// ---- host side ------------------------------------------------------------
+
+template <int kG, bool kUp, typename O>
+cudaError_t launch(const GemmI8Args& a) {
+  using F = Form<kG, kUp>;
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> resident[kMaxDevices];   // clusters at once on each device, 0 = not asked yet
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+
+  Params p;
+  memset(&p, 0, sizeof(p));
+  const int64_t N = a.d.N, K = a.d.K, E = a.d.experts;
+  if (!ffn::make_tmap(&p.tm_w, a.w, ffn::kElU8, K, E * N, kSlab, F::kCh) ||
+      (kUp && !ffn::make_tmap(&p.tm_wu, a.wu, ffn::kElU8, K, E * N, kSlab, F::kCh)) ||
+      !ffn::make_tmap(&p.tm_x, a.x, ffn::kElU8, K, a.d.M, kSlab, F::kBRows) ||
+      !ffn::make_tmap(&p.tm_x16, a.x, ffn::kElU8, K, a.d.M, kSlab, 16))
+    return cudaErrorInvalidValue;
+  p.xs = a.xs;
+  p.ws = a.ws;
+  p.wus = a.wus;
+  p.win = a.win;
+  p.y = a.y;
+  p.hdr = a.hdr;
+  p.M = a.d.M;
+  p.N = N;
+  p.nk = (int)ceil_div(K, kSlab);
+  p.tiles = (int)ceil_div(N, kG * F::kCh);
+
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(kG * std::max(1, a.num_sms / kG)), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = F::kSmem;
+  cfg.stream = a.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int workers = resident[dev].load(std::memory_order_acquire);
+  if (workers == 0) {
+    if ((err = cudaFuncSetAttribute(gemm_i8_kernel<kG, kUp, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    F::kSmem)) != cudaSuccess)
+      return err;
+    if (cudaOccupancyMaxActiveClusters(&workers, gemm_i8_kernel<kG, kUp, O>, &cfg) != cudaSuccess || workers < 1)
+      workers = std::max(1, a.num_sms / kG);
+    (void)cudaGetLastError();   // a failed query is not the launch's error
+    resident[dev].store(workers, std::memory_order_release);
+  }
+  // no more workers than the most units there can be
+  const int64_t most = (ceil_div(a.d.M, F::kRows) + (a.win.offsets ? E : 0)) * p.tiles;
+  cfg.gridDim.x = (unsigned)(kG * std::min<int64_t>(std::min(workers, std::max(1, a.num_sms / kG)), most));
+  return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<kG, kUp, O>, p);
+}
+
+template <int kG, bool kUp>
+cudaError_t launch_out(const GemmI8Args& a) {
+  return a.d.out_dtype == MOE_F32 ? launch<kG, kUp, float>(a) : launch<kG, kUp, __nv_bfloat16>(a);
+}
+
+template <int kG>
+cudaError_t launch_form(const GemmI8Args& a) {
+  return a.wu ? launch_out<kG, true>(a) : launch_out<kG, false>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_i8(const GemmI8Args& a) {
-  const int64_t nt = ceil_div(a.d.N, kTile), mt = ceil_div(a.d.M, kTile);
-  const dim3 grid((unsigned)nt, (unsigned)(mt < 64 ? mt : 64), (unsigned)a.d.experts);
-  const bool f32 = a.d.out_dtype == MOE_F32;
-  if (a.wu) {
-    if (f32) gemm_i8_kernel<true, float><<<grid, kThreads, 0, a.stream>>>(a);
-    else gemm_i8_kernel<true, __nv_bfloat16><<<grid, kThreads, 0, a.stream>>>(a);
-  } else {
-    if (f32) gemm_i8_kernel<false, float><<<grid, kThreads, 0, a.stream>>>(a);
-    else gemm_i8_kernel<false, __nv_bfloat16><<<grid, kThreads, 0, a.stream>>>(a);
-  }
-  return cudaGetLastError();
+  const int64_t fill = a.d.fill > 0 && a.d.fill < a.d.M ? a.d.fill : a.d.M;
+  return fill > 64 * a.d.experts && a.num_sms >= 2 ? launch_form<2>(a) : launch_form<1>(a);
 }
 
 }  // namespace moe
