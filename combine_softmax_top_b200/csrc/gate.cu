@@ -1,8 +1,27 @@
 // The gate: routing with softmax or sigmoid scores, a balance bias, expert
 // groups, top-k and renormalised, scaled weights; and its gradient.
 //
-// Both kernels give one warp a token and keep what belongs to its row in
-// shared memory. The choice is made in binary64 throughout.
+// gate_kernel gives one warp a token. Lane i holds `per` = ceil(E / 32)
+// consecutive experts from i * per on, so that lower lanes hold lower experts
+// and, for most groupings, a group is a whole power-of-two set of lanes. Each lane
+// sorts 32-bit keys that order like its choice values c, the low bits given
+// to the place in the lane (a sorting network of min and max, two
+// instructions a comparison), and each of the topk rounds takes the largest
+// head with one warp reduction and pops it.
+//
+// What is chosen has to be what binary64 chooses. The keys drop low bits and
+// c = s + bias carries binary32 roundings, so the chosen values (and the best
+// one left) are compared once more with the bounds of both: a token with two
+// neighbours closer than that, or with a group at the border of the open ones
+// closer than that, is done over in binary64 (choose_exactly). Without a bias
+// c is the logit itself; bf16 logits then lose nothing in the keys and need no
+// second look.
+//
+// The row is read once, 16 bytes a lane where its alignment allows.
+// gate_backward_kernel also gives one warp a token, adds the chosen experts'
+// derivatives into a row of shared memory in slot order and writes the row.
+#include <type_traits>
+
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -10,6 +29,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr uint32_t kNoKey = 0u;   // below the key of every number
+
+// 32-bit key that orders like the number
+__device__ __forceinline__ uint32_t order_key(float f) {
+  const uint32_t b = __float_as_uint(f + 0.f);   // -0 and +0 are one value
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
 
 template <typename T>
 __device__ __forceinline__ float load_logit(const T* p) {
@@ -63,39 +89,12 @@ __device__ __forceinline__ float renorm_term(float l, bool live) {
   return l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - m) / (1.f + expf(l));
 }
 
+// The choice in binary64, lane j < k returning slot j's expert. c: E doubles
+// of shared memory of this warp.
 template <typename T, bool kSigmoid>
-__global__ void __launch_bounds__(kWarps * 32)
-gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int tokens, int E, int k, int shared,
-            int renorm, moe_gate_desc g, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, Header* hdr) {
-  extern __shared__ double smem[];
+__device__ __noinline__ int choose_exactly(const T* row, const float* bias, int E, int k, moe_gate_desc g, float top,
+                                           double* c) {
   const int lane = threadIdx.x & 31;
-  double* c = smem + (threadIdx.x >> 5) * E;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= tokens) return;
-  const T* row = logits + (int64_t)t * E;
-  const int ks = k + shared;
-  int32_t* idx = topk_idx + (int64_t)t * ks;
-  float* out = topk_w + (int64_t)t * ks;
-  if (shared && lane == k) {
-    idx[k] = E;
-    out[k] = 1.f;
-  }
-  bool bad = false;
-  float top = -INFINITY;
-  for (int e = lane; e < E; e += 32) {
-    const float l = load_logit(row + e);
-    bad |= !isfinite(l) || (bias && !isfinite(bias[e]));
-    top = fmaxf(top, l);
-  }
-  if (__any_sync(kFull, bad)) {
-    if (lane < k) {
-      idx[lane] = lane;
-      out[lane] = __int_as_float(0x7fc00000);
-    }
-    if (lane == 0) latch_error(hdr, MOE_ERR_NONFINITE, (uint32_t)t);
-    return;
-  }
-  top = warp_max(top);
   double z = 1.0;
   if (!kSigmoid) {
     z = 0.0;
@@ -123,8 +122,9 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     }
     uint32_t open = 0;
     for (int j = 0; j < g.topk_groups; ++j) {
-      double v = ((open >> lane) & 1u) ? -INFINITY : rank;
-      int i = lane < g.groups && !((open >> lane) & 1u) ? lane : 64;
+      const bool free = lane < g.groups && !((open >> lane) & 1u);
+      double v = free ? rank : -INFINITY;
+      int i = free ? lane : 64;
       warp_best(v, i);
       open |= 1u << i;
     }
@@ -144,78 +144,371 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     if (lane == 0) c[i] = -INFINITY;
     __syncwarp();
   }
-  const bool live = lane < k;
-  const float l = live ? load_logit(row + sel) : 0.f;
-  float a;
-  if (renorm) {
-    a = renorm_term<kSigmoid>(l, live);
-    a /= warp_sum(a);
-  } else {
-    a = kSigmoid ? 1.f / (1.f + expf(-l)) : expf(l - top) / (float)z;
-  }
-  if (live) {
-    idx[lane] = sel;
-    out[lane] = g.scale * a;
-  }
+  return sel;
 }
 
-template <typename T, bool kSigmoid>
+// NV slots of a lane, the first `per` of them used; kBits of the key hold the slot.
+template <typename T, bool kSigmoid, int NV>
 __global__ void __launch_bounds__(kWarps * 32)
-gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ topk_idx,
-                     const float* __restrict__ grad_w, int tokens, int E, int k, int shared, int renorm, float scale,
-                     T* __restrict__ grad_logits) {
-  extern __shared__ float gsum[];
+gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int tokens, int E, int per, int k,
+            int shared, int renorm, moe_gate_desc g, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
+            Header* hdr) {
+  constexpr int kBits = NV <= 4 ? 2 : NV <= 8 ? 3 : NV <= 16 ? 4 : 5;
+  constexpr uint32_t kSlot = (1u << kBits) - 1u;
+  constexpr int kVec = 16 / sizeof(T) < NV ? 16 / sizeof(T) : NV;   // elements of a wide load
+  extern __shared__ double smem[];
   const int lane = threadIdx.x & 31;
-  float* acc = gsum + (threadIdx.x >> 5) * E;
+  double* scratch = smem + (threadIdx.x >> 5) * E;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= tokens) return;
   const T* row = logits + (int64_t)t * E;
+  const int ks = k + shared;
+  int32_t* idx = topk_idx + (int64_t)t * ks;
+  float* out = topk_w + (int64_t)t * ks;
+  const int e0 = lane * per;
+  const int mine = max(0, min(per, E - e0));   // experts of this lane
+
+  float l[NV], c[NV];   // logits, choice values
+  // wide loads where every lane's part starts on a boundary and none is cut
+  if (per == NV && E == 32 * NV) {
+#pragma unroll
+    for (int v = 0; v < NV; v += kVec) {
+      if constexpr (sizeof(T) == 4) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(row + e0 + v));
+        l[v] = q.x; l[v + 1] = q.y; l[v + 2] = q.z; l[v + 3] = q.w;
+      } else {
+        uint32_t w[kVec / 2];
+        if constexpr (kVec == 8) *reinterpret_cast<uint4*>(w) = __ldg(reinterpret_cast<const uint4*>(row + e0 + v));
+        else *reinterpret_cast<uint2*>(w) = __ldg(reinterpret_cast<const uint2*>(row + e0 + v));
+#pragma unroll
+        for (int i = 0; i < kVec / 2; ++i) {
+          l[v + 2 * i] = __uint_as_float(w[i] << 16);
+          l[v + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) l[v] = v < mine ? load_logit(row + e0 + v) : 0.f;
+  }
+  bool bad = false;
+  float top = -INFINITY;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    bad |= !isfinite(l[v]);
+    if (v < mine) top = fmaxf(top, l[v]);
+  }
+  const bool lossless = sizeof(T) == 2 && !bias;   // the keys tell all choice values apart
+  const bool scores = bias || (g.groups > 1 && g.group_best == 2);
+  float z = 1.f;
+  if (!kSigmoid) {
+    top = warp_max(top);
+    if (scores || !renorm) {
+      float part = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) part += v < mine ? expf(l[v] - top) : 0.f;
+      z = warp_sum(part);
+    }
+  }
+  // err0 + err1 |c|: bound of the difference between c (of one or of the sum of
+  // a few) and its binary64 value. Sigmoid: exp 2^-22, the sum and the
+  // quotient 2^-24 each, all at most 3 * 2^-24 of s <= 1, and the bias's sum
+  // 2^-24 |c|. Softmax: exp's argument and value, and a sum of E terms in a
+  // tree of depth <= 37: below 2^-18 of the largest score 1 / z.
+  const float err0 = bias || scores ? (kSigmoid ? 0x1p-21f : 0x1p-18f / z) : 0.f;
+  const float err1 = bias ? 0x1p-22f : 0.f;
+  bool unsure = false;
+  if (scores) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) c[v] = kSigmoid ? 1.f / (1.f + expf(-l[v])) : expf(l[v] - top) / z;
+    if (bias) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v < mine) {
+          const float b = __ldg(bias + e0 + v);
+          bad |= !isfinite(b);
+          c[v] += b;
+        }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) c[v] = l[v];
+  }
+  if (__any_sync(kFull, bad)) {
+    if (lane < ks) {
+      idx[lane] = lane < k ? lane : E;
+      out[lane] = lane < k ? __int_as_float(0x7fc00000) : 1.f;
+    }
+    if (lane == 0) latch_error(hdr, MOE_ERR_NONFINITE, (uint32_t)t);
+    return;
+  }
+
+  // groups: `closed` has bit v where slot v's group is not open
+  uint32_t closed = 0;
+  if (g.groups > 1) {
+    const int n = E / g.groups;
+    float b1 = -INFINITY, b2 = -INFINITY;
+    auto take = [&](float v) {
+      b2 = fmaxf(b2, fminf(b1, v));
+      b1 = fmaxf(b1, v);
+    };
+    const int span = n / per;   // lanes of a group
+    const bool lanes = span * per == n && (span & (span - 1)) == 0;
+    if (lanes) {   // a group is an aligned set of lanes (and all of them are full)
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v < mine) take(c[v]);
+      for (int off = 1; off < span; off <<= 1) {
+        const float o1 = __shfl_xor_sync(kFull, b1, off), o2 = __shfl_xor_sync(kFull, b2, off);
+        b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+        b1 = fmaxf(b1, o1);
+      }
+    } else {       // any other grouping: lane i looks at group i
+      float* row_c = reinterpret_cast<float*>(scratch);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v < mine) row_c[e0 + v] = c[v];
+      __syncwarp();
+      if (lane < g.groups)
+        for (int i = 0; i < n; ++i) take(row_c[lane * n + i]);
+      __syncwarp();
+    }
+    const bool two = g.group_best == 2;
+    const float r = two ? b1 + b2 : b1;
+    const float e = two ? 2.f * err0 + err1 * (fabsf(b1) + fabsf(b2)) + 0x1p-23f * fabsf(r)
+                        : err0 + err1 * fabsf(b1);
+    const float lo = r - e, hi = r + e;
+    // lane i: whether its group (lanes: the one it belongs to) is open: fewer
+    // than topk_groups others may be above it
+    const int gi = lanes ? lane / span : lane;
+    int above = 0, may = 0;
+    for (int h = 0; h < g.groups; ++h) {
+      const int src = lanes ? h * span : h;
+      const float olo = __shfl_sync(kFull, lo, src), ohi = __shfl_sync(kFull, hi, src);
+      if (e == 0.f) {   // exact: ties to the lowest group
+        above += olo > r || (olo == r && h < gi);
+        may = above;
+      } else if (h != gi) {
+        above += olo > hi;
+        may += !(ohi < lo);
+      }
+    }
+    const bool open = may < g.topk_groups;
+    unsure = gi < g.groups && !open && above < g.topk_groups;
+    const uint32_t opens = __ballot_sync(kFull, gi < g.groups && open);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int src = lanes ? lane : (e0 + v < E ? (e0 + v) / n : 0);
+      if (!((opens >> src) & 1u)) closed |= 1u << v;
+    }
+    if (!bias && scores) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) c[v] = l[v];   // the groups' scores only ranked the groups
+    }
+  }
+
+  uint32_t key[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    key[v] = v < mine && !((closed >> v) & 1u) ? (order_key(c[v]) & ~kSlot) | (kSlot - v) : kNoKey;
+  // odd-even merge sort, descending
+#pragma unroll
+  for (int p = 1; p < NV; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < NV; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (j + i + q < NV && (j + i) / (2 * p) == (j + i + q) / (2 * p)) {
+            const uint32_t a = key[j + i], b = key[j + i + q];
+            key[j + i] = max(a, b);
+            key[j + i + q] = min(a, b);
+          }
+  int sel = 0;   // lane j: slot j's expert (lane k: the best one left, or -1)
+  const int rounds = lossless ? k : min(k + 1, 32);
+  for (int j = 0; j < rounds; ++j) {
+    const uint32_t head = key[0] & ~kSlot;
+    const uint32_t m = __reduce_max_sync(kFull, head);
+    const int who = __ffs(__ballot_sync(kFull, head == m)) - 1;   // lowest lane: lowest expert
+    const int e = __shfl_sync(kFull, e0 + (int)(kSlot - (key[0] & kSlot)), who);
+    if (lane == j) sel = m == kNoKey ? -1 : e;
+    if (lane == who) {
+#pragma unroll
+      for (int v = 0; v + 1 < NV; ++v) key[v] = key[v + 1];
+      key[NV - 1] = kNoKey;
+    }
+  }
+  if (!lossless) {
+    // neighbours in order beyond doubt? (k = 32 has no lane for the best one
+    // left: the remaining heads stand for it)
+    const bool have = lane < rounds && sel >= 0;
+    float v = have ? load_logit(row + sel) : -INFINITY;
+    if (bias && have) v = (kSigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / z) + __ldg(bias + sel);
+    const float next = __shfl_down_sync(kFull, v, 1);
+    const int nsel = __shfl_down_sync(kFull, sel, 1);
+    const float mag = fmaxf(fmaxf(fabsf(v), fabsf(next)), 0x1p-126f);
+    const float cut = ldexpf(mag, kBits - 23);   // what the keys drop
+    if (bias) {
+      const float near = 2.f * (err0 + err1 * mag) + cut;
+      if (lane < k && lane + 1 < rounds && nsel >= 0) unsure |= !(v - next > near);
+    } else {
+      if (lane + 1 < k) unsure |= !(v > next || (v == next && sel < nsel));
+      if (lane == k - 1 && lane + 1 < rounds && nsel >= 0) unsure |= !(v - next > cut);
+    }
+    if (rounds == k) {   // k = 32
+      const uint32_t left = __reduce_max_sync(kFull, key[0]);
+      const float last = __shfl_sync(kFull, v, k - 1);
+      const float near = bias ? 2.f * (err0 + err1 * fabsf(last)) : 0.f;
+      unsure |= left != kNoKey && !(order_key(last - near - ldexpf(fmaxf(fabsf(last), 0x1p-126f), kBits - 23)) > (left | kSlot));
+    }
+    if (__any_sync(kFull, unsure)) {
+      top = warp_max(top);
+      __syncwarp();
+      sel = choose_exactly<T, kSigmoid>(row, bias, E, k, g, top, scratch);
+    }
+  } else if (__any_sync(kFull, unsure)) {
+    top = warp_max(top);
+    __syncwarp();
+    sel = choose_exactly<T, kSigmoid>(row, bias, E, k, g, top, scratch);
+  }
+
+  const bool live = lane < k;
+  const float lj = live ? load_logit(row + sel) : 0.f;
+  float a;
+  if (renorm) {
+    a = renorm_term<kSigmoid>(lj, live);
+    a /= warp_sum(a);
+  } else {
+    a = kSigmoid ? 1.f / (1.f + expf(-lj)) : expf(lj - top) / z;
+  }
+  if (lane < ks) {
+    idx[lane] = live ? sel : E;
+    out[lane] = live ? g.scale * a : 1.f;
+  }
+}
+
+// 16 bytes of a row of grad_logits at a time where its alignment allows.
+template <typename T, bool kSigmoid, bool kRenorm>
+__global__ void __launch_bounds__(kWarps * 32)
+gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ topk_idx,
+                     const float* __restrict__ grad_w, int tokens, int E, int k, int shared, float scale,
+                     T* __restrict__ grad_logits) {
+  constexpr int kVec = 16 / sizeof(T);
+  constexpr bool kEvery = !kSigmoid && !kRenorm;   // every logit has a gradient
+  extern __shared__ float4 gsum4[];
+  const int lane = threadIdx.x & 31;
+  const int pad = (E + 7) / 8 * 8;
+  float* acc = reinterpret_cast<float*>(gsum4) + (threadIdx.x >> 5) * pad;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= tokens) return;
+  const T* row = logits + (int64_t)t * E;
+  T* grow = grad_logits + (int64_t)t * E;
+  const bool vec = E % kVec == 0;
   const int ks = k + shared;
   int e = -1;
   float gw = 0.f, l = 0.f;
   if (lane < k) {
     e = topk_idx[(int64_t)t * ks + lane];
-    if (e >= 0 && e < E) {
-      gw = scale * grad_w[(int64_t)t * ks + lane];
-      l = load_logit(row + e);
-    } else {
-      e = -1;
-    }
+    gw = scale * grad_w[(int64_t)t * ks + lane];
   }
-  const bool live = e >= 0;
-  float top = 0.f, z = 1.f, d;   // d: what slot `lane` adds to its expert
-  const bool every = !kSigmoid && !renorm;
-  if (every) {
-    top = -INFINITY;
-    for (int i = lane; i < E; i += 32) top = fmaxf(top, load_logit(row + i));
-    top = warp_max(top);
-    z = 0.f;
-    for (int i = lane; i < E; i += 32) z += expf(load_logit(row + i) - top);
+  const bool live = e >= 0 && e < E;
+  if (live) l = load_logit(row + e);
+  else gw = 0.f;
+  for (int i = 4 * lane; i < pad; i += 128) *reinterpret_cast<float4*>(acc + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+  // kVec elements of the row
+  auto load = [&](int i, float (&v)[kVec]) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(row + i));
+      v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + i));
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        v[2 * b] = __uint_as_float(w[b] << 16);
+        v[2 * b + 1] = __uint_as_float(w[b] & 0xFFFF0000u);
+      }
+    }
+  };
+  auto store = [&](int i, const float (&v)[kVec]) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(grow + i) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * b], v[2 * b + 1]);
+        w[b] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      *reinterpret_cast<uint4*>(grow + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  };
+  float top = -INFINITY, z = 0.f, d;   // d: what slot `lane` adds to its expert
+  if constexpr (kEvery) {
+    if (vec) {
+      for (int i = lane * kVec; i < E; i += 32 * kVec) {
+        float v[kVec];
+        load(i, v);
+#pragma unroll
+        for (int b = 0; b < kVec; ++b) top = fmaxf(top, v[b]);
+      }
+      top = warp_max(top);
+      for (int i = lane * kVec; i < E; i += 32 * kVec) {
+        float v[kVec];
+        load(i, v);
+#pragma unroll
+        for (int b = 0; b < kVec; ++b) z += expf(v[b] - top);
+      }
+    } else {
+      for (int i = lane; i < E; i += 32) top = fmaxf(top, load_logit(row + i));
+      top = warp_max(top);
+      for (int i = lane; i < E; i += 32) z += expf(load_logit(row + i) - top);
+    }
     z = warp_sum(z);
     d = gw;
   } else {
-    float q = renorm ? renorm_term<kSigmoid>(l, live) : 1.f / (1.f + expf(-l));
+    float q = kRenorm ? renorm_term<kSigmoid>(l, live) : 1.f / (1.f + expf(-l));
     float gd = gw;
-    if (renorm) {
+    if (kRenorm) {
       const float s = warp_sum(q);
-      q = s > 0.f || s != s ? q / s : 0.f;   // no slot takes part: 0
+      q = s == 0.f ? 0.f : q / s;   // 0: no slot takes part
       gd -= warp_sum(q * gw);
     }
     d = q * gd;
     if (kSigmoid) d *= 1.f / (1.f + expf(l));
   }
-  for (int i = lane; i < E; i += 32) acc[i] = 0.f;
   __syncwarp();
-  for (int j = 0; j < k; ++j) {   // slot order: an expert named twice sums in a fixed order
-    if (lane == j && live) acc[e] += d;
-    __syncwarp();
-  }
-  if (every) {
-    const float dot = warp_sum(live ? gw * (expf(l - top) / z) : 0.f);
-    for (int i = lane; i < E; i += 32)
-      store_grad(grad_logits + (int64_t)t * E + i, expf(load_logit(row + i) - top) / z * (acc[i] - dot));
+  // an expert named twice sums in slot order; nearly always none is
+  const uint32_t same = __match_any_sync(kFull, live ? e : ~lane);
+  if (!__any_sync(kFull, (same & (same - 1u)) != 0u)) {
+    if (live) acc[e] = d;
   } else {
-    for (int i = lane; i < E; i += 32) store_grad(grad_logits + (int64_t)t * E + i, acc[i]);
+    for (int j = 0; j < k; ++j) {
+      if (lane == j && live) acc[e] += d;
+      __syncwarp();
+    }
+  }
+  __syncwarp();
+  const float dot = kEvery ? warp_sum(live ? gw * (expf(l - top) / z) : 0.f) : 0.f;
+  if (vec) {
+    for (int i = lane * kVec; i < E; i += 32 * kVec) {
+      float v[kVec], r[kVec];
+      if constexpr (kEvery) load(i, v);
+#pragma unroll
+      for (int b = 0; b < kVec; b += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(acc + i + b);
+        r[b] = a.x; r[b + 1] = a.y; r[b + 2] = a.z; r[b + 3] = a.w;
+      }
+      if constexpr (kEvery) {
+#pragma unroll
+        for (int b = 0; b < kVec; ++b) r[b] = expf(v[b] - top) / z * (r[b] - dot);
+      }
+      store(i, r);
+    }
+  } else {
+    for (int i = lane; i < E; i += 32)
+      store_grad(grow + i, kEvery ? expf(load_logit(row + i) - top) / z * (acc[i] - dot) : acc[i]);
   }
 }
 
@@ -223,41 +516,44 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
 
 cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits, const float* bias, int32_t* idx,
                         float* w) {
-  const int T = (int)c.s.T, E = (int)c.routed_E, k = (int)c.routed_k;
+  const int T = (int)c.s.T, E = (int)c.routed_E, k = (int)c.routed_k, per = (E + 31) / 32;
   const dim3 grid((T + kWarps - 1) / kWarps);
   const size_t smem = (size_t)kWarps * E * sizeof(double);   // <= 32 KB
   auto go = [&](auto kernel, auto* l) {
-    kernel<<<grid, kWarps * 32, smem, c.stream>>>(l, bias, T, E, k, c.shared, c.s.renorm, g, idx, w, c.ws.hdr);
+    kernel<<<grid, kWarps * 32, smem, c.stream>>>(l, bias, T, E, per, k, c.shared, c.s.renorm, g, idx, w, c.ws.hdr);
     return cudaGetLastError();
   };
-  const bool sig = g.score == MOE_SCORE_SIGMOID;
-  if (g.logits_dtype == MOE_BF16) {
-    const __nv_bfloat16* l = (const __nv_bfloat16*)logits;
-    return sig ? go(gate_kernel<__nv_bfloat16, true>, l) : go(gate_kernel<__nv_bfloat16, false>, l);
-  }
-  const float* l = (const float*)logits;
-  return sig ? go(gate_kernel<float, true>, l) : go(gate_kernel<float, false>, l);
+  auto by_size = [&](auto* l, auto sig) {
+    using L = std::remove_const_t<std::remove_pointer_t<decltype(l)>>;
+    constexpr bool kSig = decltype(sig)::value;
+    if (per <= 4) return go(gate_kernel<L, kSig, 4>, l);
+    if (per <= 8) return go(gate_kernel<L, kSig, 8>, l);
+    if (per <= 16) return go(gate_kernel<L, kSig, 16>, l);
+    return go(gate_kernel<L, kSig, 32>, l);
+  };
+  auto by_score = [&](auto* l) {
+    return g.score == MOE_SCORE_SIGMOID ? by_size(l, std::true_type()) : by_size(l, std::false_type());
+  };
+  return g.logits_dtype == MOE_BF16 ? by_score((const __nv_bfloat16*)logits) : by_score((const float*)logits);
 }
 
 cudaError_t launch_gate_backward(const moe_shape& s, const moe_gate_desc& g, const void* logits, const int32_t* idx,
                                  const float* grad_w, void* grad_logits, cudaStream_t stream) {
   const int T = (int)s.T, E = (int)s.E, k = (int)s.topk, shared = (s.flags & MOE_FLAG_SHARED_EXPERT) ? 1 : 0;
   const dim3 grid((T + kWarps - 1) / kWarps);
-  const size_t smem = (size_t)kWarps * E * sizeof(float);
+  const size_t smem = (size_t)kWarps * ((E + 7) / 8 * 8) * sizeof(float);
   auto go = [&](auto kernel, auto* l, auto* d) {
-    kernel<<<grid, kWarps * 32, smem, stream>>>(l, idx, grad_w, T, E, k, shared, s.renorm, g.scale, d);
+    kernel<<<grid, kWarps * 32, smem, stream>>>(l, idx, grad_w, T, E, k, shared, g.scale, d);
     return cudaGetLastError();
   };
-  const bool sig = g.score == MOE_SCORE_SIGMOID;
-  if (g.logits_dtype == MOE_BF16) {
-    const __nv_bfloat16* l = (const __nv_bfloat16*)logits;
-    __nv_bfloat16* d = (__nv_bfloat16*)grad_logits;
-    return sig ? go(gate_backward_kernel<__nv_bfloat16, true>, l, d)
-               : go(gate_backward_kernel<__nv_bfloat16, false>, l, d);
-  }
-  const float* l = (const float*)logits;
-  float* d = (float*)grad_logits;
-  return sig ? go(gate_backward_kernel<float, true>, l, d) : go(gate_backward_kernel<float, false>, l, d);
+  auto by_form = [&](auto* l, auto* d) {
+    using L = std::remove_pointer_t<decltype(d)>;
+    if (g.score == MOE_SCORE_SIGMOID)
+      return s.renorm ? go(gate_backward_kernel<L, true, true>, l, d) : go(gate_backward_kernel<L, true, false>, l, d);
+    return s.renorm ? go(gate_backward_kernel<L, false, true>, l, d) : go(gate_backward_kernel<L, false, false>, l, d);
+  };
+  return g.logits_dtype == MOE_BF16 ? by_form((const __nv_bfloat16*)logits, (__nv_bfloat16*)grad_logits)
+                                    : by_form((const float*)logits, (float*)grad_logits);
 }
 
 }  // namespace moe

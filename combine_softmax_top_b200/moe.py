@@ -298,54 +298,61 @@ def make_gate(score: str = "softmax", groups: int = 1, topk_groups: int = 1, gro
     return moe_gate_desc(_SCORES[score], _DT[logits], groups, topk_groups, group_best, scale)
 
 
-def _dense(fn: str, name: str, t, shape, *dtypes) -> None:
-    """A contiguous tensor on the current device of this shape and one of
+def _begin(fn: str, name: str, t, stream):
+    """(current device, stream handle) of a call whose first tensor is t."""
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must be on the current CUDA device, is on {t.device}")
+    dev = torch.cuda.current_device()
+    return dev, (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+
+
+def _dense(fn: str, name: str, t, shape, dtypes, dev: int) -> int:
+    """Address of a contiguous tensor on device `dev` of this shape and one of
     these dtypes, as the library reads it; anything else raises."""
-    if (t is None or not t.is_cuda or t.get_device() != torch.cuda.current_device() or not t.is_contiguous()
-            or tuple(t.shape) != tuple(shape) or t.dtype not in dtypes):
+    if (t is None or t.dtype not in dtypes or t.shape != shape or t.get_device() != dev or not t.is_contiguous()):
         got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}"
         raise ValueError(f"{fn}: {name} must be a contiguous tensor on the current CUDA device, of shape "
                          f"{tuple(shape)} and dtype {' or '.join(str(d) for d in dtypes)}, got {got}")
+    return t.data_ptr()
 
 
-def _gate_args(fn, shape, gate, logits, topk_idx, w) -> None:
+_F32, _I32, _I8 = (torch.float32,), (torch.int32,), (torch.int8,)
+_FLOATS = (torch.float32, torch.bfloat16)
+_SRC = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _gate_args(fn, shape, gate, logits, topk_idx, w, dev):
     ks = shape.topk + (shape.flags & 1)
-    dt = torch.bfloat16 if gate.logits_dtype == MOE_BF16 else torch.float32
-    _dense(fn, "logits", logits, (shape.T, shape.E), dt)
-    _dense(fn, "topk_idx", topk_idx, (shape.T, ks), torch.int32)
-    _dense(fn, "topk weights", w, (shape.T, ks), torch.float32)
+    return (_dense(fn, "logits", logits, (shape.T, shape.E), _FLOATS[gate.logits_dtype:gate.logits_dtype + 1], dev),
+            _dense(fn, "topk_idx", topk_idx, (shape.T, ks), _I32, dev),
+            _dense(fn, "topk weights", w, (shape.T, ks), _F32, dev))
 
 
 def moe_gate(shape, gate: moe_gate_desc, logits, bias, topk_idx, topk_w, ws, stream=None) -> None:
     """Routing by scores, an optional balance bias [E] and expert groups
     (moe_gate in include/moe.h); outputs as moe_route's."""
-    _gate_args("moe_gate", shape, gate, logits, topk_idx, topk_w)
-    if bias is not None:
-        _dense("moe_gate", "bias", bias, (shape.E,), torch.float32)
-    _check("moe_gate", lib().moe_gate(ctypes.byref(shape), ctypes.byref(gate), _ptr(logits), _ptr(bias),
-                                      _ptr(topk_idx), _ptr(topk_w), _ptr(ws), _stream(stream)))
+    fn = "moe_gate"
+    dev, st = _begin(fn, "logits", logits, stream)
+    pl, pi, pw = _gate_args(fn, shape, gate, logits, topk_idx, topk_w, dev)
+    pb = None if bias is None else _dense(fn, "bias", bias, (shape.E,), _F32, dev)
+    _check(fn, lib().moe_gate(ctypes.byref(shape), ctypes.byref(gate), pl, pb, pi, pw, ws.data_ptr(), st))
 
 
 def moe_gate_backward(shape, gate: moe_gate_desc, logits, topk_idx, grad_w, grad_logits, stream=None) -> None:
     """grad_logits [T, E] from the gradient of moe_gate's weights."""
-    _gate_args("moe_gate_backward", shape, gate, logits, topk_idx, grad_w)
-    _dense("moe_gate_backward", "grad_logits", grad_logits, logits.shape, logits.dtype)
-    _check("moe_gate_backward", lib().moe_gate_backward(ctypes.byref(shape), ctypes.byref(gate), _ptr(logits),
-                                                        _ptr(topk_idx), _ptr(grad_w), _ptr(grad_logits),
-                                                        _stream(stream)))
+    fn = "moe_gate_backward"
+    dev, st = _begin(fn, "logits", logits, stream)
+    pl, pi, pw = _gate_args(fn, shape, gate, logits, topk_idx, grad_w, dev)
+    pg = _dense(fn, "grad_logits", grad_logits, logits.shape, (logits.dtype,), dev)
+    _check(fn, lib().moe_gate_backward(ctypes.byref(shape), ctypes.byref(gate), pl, pi, pw, pg, st))
 
 
-_SRC = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
-
-
-def _windows(fn, offsets, counts) -> int:
-    """Number of windows (0: all rows)."""
+def _windows(fn, offsets, counts, dev):
+    """Windows of a call: (how many, address of offsets, of counts); (0, None, None) for all rows."""
     if offsets is None and counts is None:
-        return 0
+        return 0, None, None
     n = 0 if offsets is None else offsets.numel()
-    _dense(fn, "offsets", offsets, (n,), torch.int32)
-    _dense(fn, "counts", counts, (n,), torch.int32)
-    return n
+    return n, _dense(fn, "offsets", offsets, (n,), _I32, dev), _dense(fn, "counts", counts, (n,), _I32, dev)
 
 
 def moe_quant_i8(x, q, scale, offsets=None, counts=None, stream=None) -> None:
@@ -354,12 +361,13 @@ def moe_quant_i8(x, q, scale, offsets=None, counts=None, stream=None) -> None:
     fn = "moe_quant_i8"
     if x.dim() != 2:
         raise ValueError(f"{fn}: x must be [rows, cols], got {tuple(x.shape)}")
-    _dense(fn, "x", x, x.shape, torch.float32, torch.bfloat16)
-    _dense(fn, "q", q, x.shape, torch.int8)
-    _dense(fn, "scale", scale, x.shape[:1], torch.float32)
-    n = _windows(fn, offsets, counts)
-    _check(fn, lib().moe_quant_i8(x.shape[0], x.shape[1], _SRC[x.dtype], _ptr(x), n, _ptr(offsets), _ptr(counts),
-                                  _ptr(q), _ptr(scale), _stream(stream)))
+    dev, st = _begin(fn, "x", x, stream)
+    rows, cols = x.shape
+    px = _dense(fn, "x", x, x.shape, _FLOATS, dev)
+    n, po, pc = _windows(fn, offsets, counts, dev)
+    _check(fn, lib().moe_quant_i8(rows, cols, _SRC[x.dtype], px, n, po, pc,
+                                  _dense(fn, "q", q, x.shape, _I8, dev),
+                                  _dense(fn, "scale", scale, (rows,), _F32, dev), st))
 
 
 def moe_gemm_i8(x, x_scale, w, w_scale, y, ws, w_up=None, up_scale=None, offsets=None, counts=None,
@@ -371,21 +379,22 @@ def moe_gemm_i8(x, x_scale, w, w_scale, y, ws, w_up=None, up_scale=None, offsets
     fn = "moe_gemm_i8"
     if x.dim() != 2 or w.dim() not in (2, 3):
         raise ValueError(f"{fn}: x must be [M, K] and w [N, K] or [E, N, K], got {tuple(x.shape)}, {tuple(w.shape)}")
-    n = _windows(fn, offsets, counts)
-    E = w.shape[0] if w.dim() == 3 else 1
+    dev, st = _begin(fn, "x", x, stream)
+    (M, K), wshape = x.shape, w.shape
+    N, E = wshape[-2], wshape[0] if len(wshape) == 3 else 1
+    n, po, pc = _windows(fn, offsets, counts, dev)
     if n and n != E:
         raise ValueError(f"{fn}: {n} windows for the weights of {E} experts")
-    d = moe_gemm_i8_desc(x.shape[0], w.shape[-2], x.shape[1], E, fill, _SRC.get(y.dtype, -1), 0)
-    _dense(fn, "x", x, x.shape, torch.int8)
-    _dense(fn, "x_scale", x_scale, (d.M,), torch.float32)
-    _dense(fn, "w", w, w.shape[:-1] + (d.K,), torch.int8)
-    _dense(fn, "w_scale", w_scale, w.shape[:-1], torch.float32)
+    px, pxs = _dense(fn, "x", x, (M, K), _I8, dev), _dense(fn, "x_scale", x_scale, (M,), _F32, dev)
+    pw = _dense(fn, "w", w, (*wshape[:-1], K), _I8, dev)
+    pws = _dense(fn, "w_scale", w_scale, wshape[:-1], _F32, dev)
+    pu = pus = None
     if w_up is not None or up_scale is not None:
-        _dense(fn, "w_up", w_up, w.shape, torch.int8)
-        _dense(fn, "up_scale", up_scale, w_scale.shape, torch.float32)
-    _dense(fn, "y", y, (d.M, d.N), torch.bfloat16, torch.float32)
-    _check(fn, lib().moe_gemm_i8(ctypes.byref(d), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(w_up),
-                                 _ptr(up_scale), _ptr(offsets), _ptr(counts), _ptr(y), _ptr(ws), _stream(stream)))
+        pu = _dense(fn, "w_up", w_up, wshape, _I8, dev)
+        pus = _dense(fn, "up_scale", up_scale, wshape[:-1], _F32, dev)
+    py = _dense(fn, "y", y, (M, N), _FLOATS, dev)
+    d = moe_gemm_i8_desc(M, N, K, E, fill, _SRC[y.dtype], 0)
+    _check(fn, lib().moe_gemm_i8(ctypes.byref(d), px, pxs, pw, pws, pu, pus, po, pc, py, ws.data_ptr(), st))
 
 
 def moe_dispatch_noalloc(shape, x, topk_idx, bufs: moe_dispatch_bufs, stream=None) -> None:

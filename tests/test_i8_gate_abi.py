@@ -111,9 +111,9 @@ def test_gemm_refusals(over, code):
 def test_python_binding_refuses_what_the_library_cannot_see():
     """Tensors off the device, strided, or of another type or shape."""
     x = torch.zeros(4, 128, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="moe_quant_i8: x must be"):
+    with pytest.raises(ValueError, match="moe_quant_i8: x must be on the current CUDA device"):
         moe.moe_quant_i8(x, torch.zeros(4, 128, dtype=torch.int8), torch.zeros(4))
-    with pytest.raises(ValueError, match="moe_gemm_i8: 3 windows|offsets"):
+    with pytest.raises(ValueError, match="moe_gemm_i8: x must be on the current CUDA device"):
         moe.moe_gemm_i8(x, None, torch.zeros(2, 8, 128, dtype=torch.int8), None, x, None,
                         offsets=torch.zeros(3, dtype=torch.int32), counts=torch.zeros(3, dtype=torch.int32))
     with pytest.raises(ValueError, match="x must be"):
