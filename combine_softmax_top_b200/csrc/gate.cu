@@ -17,7 +17,7 @@
 // c is the logit itself; bf16 logits then lose nothing in the keys and need no
 // second look.
 //
-// The row is read once, 16 bytes a lane where its alignment allows.
+// The row is read once, four elements at a time where its alignment allows.
 // gate_backward_kernel also gives one warp a token, adds the chosen experts'
 // derivatives into a row of shared memory in slot order and writes the row.
 #include <type_traits>
@@ -47,6 +47,26 @@ template <typename T>
 __device__ __forceinline__ void store_grad(T* p, float v) {
   if constexpr (sizeof(T) == 2) *p = __float2bfloat16_rn(v);
   else *p = v;
+}
+
+// four elements at an address that is a multiple of their size
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+  const float4 q = __ldg(reinterpret_cast<const float4*>(p));
+  v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
+  const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+  v[0] = __uint_as_float(q.x << 16);
+  v[1] = __uint_as_float(q.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(q.y << 16);
+  v[3] = __uint_as_float(q.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -155,7 +175,6 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
             Header* hdr) {
   constexpr int kBits = NV <= 4 ? 2 : NV <= 8 ? 3 : NV <= 16 ? 4 : 5;
   constexpr uint32_t kSlot = (1u << kBits) - 1u;
-  constexpr int kVec = 16 / sizeof(T) < NV ? 16 / sizeof(T) : NV;   // elements of a wide load
   extern __shared__ double smem[];
   const int lane = threadIdx.x & 31;
   double* scratch = smem + (threadIdx.x >> 5) * E;
@@ -172,20 +191,11 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
   // wide loads where every lane's part starts on a boundary and none is cut
   if (per == NV && E == 32 * NV) {
 #pragma unroll
-    for (int v = 0; v < NV; v += kVec) {
-      if constexpr (sizeof(T) == 4) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(row + e0 + v));
-        l[v] = q.x; l[v + 1] = q.y; l[v + 2] = q.z; l[v + 3] = q.w;
-      } else {
-        uint32_t w[kVec / 2];
-        if constexpr (kVec == 8) *reinterpret_cast<uint4*>(w) = __ldg(reinterpret_cast<const uint4*>(row + e0 + v));
-        else *reinterpret_cast<uint2*>(w) = __ldg(reinterpret_cast<const uint2*>(row + e0 + v));
+    for (int v = 0; v < NV; v += 4) {
+      float q[4];
+      load4(row + e0 + v, q);
 #pragma unroll
-        for (int i = 0; i < kVec / 2; ++i) {
-          l[v + 2 * i] = __uint_as_float(w[i] << 16);
-          l[v + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-      }
+      for (int b = 0; b < 4; ++b) l[v + b] = q[b];
     }
   } else {
 #pragma unroll
@@ -325,49 +335,74 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
             key[j + i] = max(a, b);
             key[j + i + q] = min(a, b);
           }
-  int sel = 0;   // lane j: slot j's expert (lane k: the best one left, or -1)
-  const int rounds = lossless ? k : min(k + 1, 32);
-  for (int j = 0; j < rounds; ++j) {
+  int sel = -1;   // lane j: slot j's expert (lane k: the best one left, or -1)
+  auto pop = [&](int j) -> uint32_t {   // the largest head, into lane j
     const uint32_t head = key[0] & ~kSlot;
     const uint32_t m = __reduce_max_sync(kFull, head);
     const int who = __ffs(__ballot_sync(kFull, head == m)) - 1;   // lowest lane: lowest expert
     const int e = __shfl_sync(kFull, e0 + (int)(kSlot - (key[0] & kSlot)), who);
-    if (lane == j) sel = m == kNoKey ? -1 : e;
+    if (lane == j && m != kNoKey) sel = e;
     if (lane == who) {
 #pragma unroll
       for (int v = 0; v + 1 < NV; ++v) key[v] = key[v + 1];
       key[NV - 1] = kNoKey;
     }
-  }
-  if (!lossless) {
-    // neighbours in order beyond doubt? (k = 32 has no lane for the best one
-    // left: the remaining heads stand for it)
-    const bool have = lane < rounds && sel >= 0;
-    float v = have ? load_logit(row + sel) : -INFINITY;
-    if (bias && have) v = (kSigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / z) + __ldg(bias + sel);
+    return m;
+  };
+  const int rounds = lossless ? k : min(k + 1, 32);
+  for (int j = 0; j < rounds; ++j) pop(j);
+  unsure = __any_sync(kFull, unsure);   // which groups are open
+  if (!lossless && !unsure) {
+    float v = sel >= 0 ? load_logit(row + sel) : -INFINITY;
+    if (bias && sel >= 0) v = (kSigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / z) + __ldg(bias + sel);
     const float next = __shfl_down_sync(kFull, v, 1);
     const int nsel = __shfl_down_sync(kFull, sel, 1);
-    const float mag = fmaxf(fmaxf(fabsf(v), fabsf(next)), 0x1p-126f);
+    const float mag = fmaxf(fmaxf(fabsf(v), sel >= 0 && nsel >= 0 ? fabsf(next) : 0.f), 0x1p-126f);
     const float cut = ldexpf(mag, kBits - 23);   // what the keys drop
-    if (bias) {
-      const float near = 2.f * (err0 + err1 * mag) + cut;
-      if (lane < k && lane + 1 < rounds && nsel >= 0) unsure |= !(v - next > near);
-    } else {
-      if (lane + 1 < k) unsure |= !(v > next || (v == next && sel < nsel));
-      if (lane == k - 1 && lane + 1 < rounds && nsel >= 0) unsure |= !(v - next > cut);
+    const float near = 2.f * (err0 + err1 * mag) + cut;
+    bool doubt = false;   // between lanes j and j + 1
+    if (lane + 1 < k) doubt = bias ? !(v - next > near) : !(v > next || (v == next && sel < nsel));
+    if (lane == k - 1) doubt = k == 32 || (nsel >= 0 && !(v - next > near));
+    if (__any_sync(kFull, doubt)) {
+      // pop whatever may reach the last slot
+      const uint32_t lim = order_key(__shfl_sync(kFull, v - near, k - 1));
+      int n = rounds;
+      uint32_t m = __reduce_max_sync(kFull, key[0]);
+      while (n < 32 && m != kNoKey && (m | kSlot) >= lim) {
+        pop(n++);
+        m = __reduce_max_sync(kFull, key[0]);
+      }
+      unsure = m != kNoKey && (m | kSlot) >= lim;   // more than a warp of them
+      if (!unsure) {
+        double zd = 1.0;
+        if (!kSigmoid && bias) {
+          double part = 0.0;
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (i < mine) part += exp((double)l[i] - (double)top);
+          zd = warp_sum(part);
+        }
+        double c64 = -INFINITY;
+        if (sel >= 0) {
+          const double x = load_logit(row + sel);
+          c64 = !bias ? x
+                      : (kSigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top) / zd) + (double)__ldg(bias + sel);
+        }
+        int rank = 0;
+        for (int i = 0; i < n; ++i) {
+          const double o = __shfl_sync(kFull, c64, i);
+          const int os = __shfl_sync(kFull, sel, i);
+          rank += o > c64 || (o == c64 && os < sel);
+        }
+        int* slots = reinterpret_cast<int*>(scratch);
+        __syncwarp();
+        if (sel >= 0 && rank < k) slots[rank] = sel;
+        __syncwarp();
+        if (lane < k) sel = slots[lane];
+      }
     }
-    if (rounds == k) {   // k = 32
-      const uint32_t left = __reduce_max_sync(kFull, key[0]);
-      const float last = __shfl_sync(kFull, v, k - 1);
-      const float near = bias ? 2.f * (err0 + err1 * fabsf(last)) : 0.f;
-      unsure |= left != kNoKey && !(order_key(last - near - ldexpf(fmaxf(fabsf(last), 0x1p-126f), kBits - 23)) > (left | kSlot));
-    }
-    if (__any_sync(kFull, unsure)) {
-      top = warp_max(top);
-      __syncwarp();
-      sel = choose_exactly<T, kSigmoid>(row, bias, E, k, g, top, scratch);
-    }
-  } else if (__any_sync(kFull, unsure)) {
+  }
+  if (unsure) {
     top = warp_max(top);
     __syncwarp();
     sel = choose_exactly<T, kSigmoid>(row, bias, E, k, g, top, scratch);
@@ -388,23 +423,23 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
   }
 }
 
-// 16 bytes of a row of grad_logits at a time where its alignment allows.
-template <typename T, bool kSigmoid, bool kRenorm>
+// Lane i holds elements (32 c + i) kW .. + kW - 1 of the row, c < NV / kW:
+// kW = 4 where rows start on a boundary of four elements, else 1. The row is
+// read only for a softmax that is not renormalised, where every logit has a
+// gradient, and then once.
+template <typename T, bool kSigmoid, bool kRenorm, int NV, int kW>
 __global__ void __launch_bounds__(kWarps * 32)
 gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ topk_idx,
                      const float* __restrict__ grad_w, int tokens, int E, int k, int shared, float scale,
                      T* __restrict__ grad_logits) {
-  constexpr int kVec = 16 / sizeof(T);
-  constexpr bool kEvery = !kSigmoid && !kRenorm;   // every logit has a gradient
-  extern __shared__ float4 gsum4[];
+  constexpr bool kEvery = !kSigmoid && !kRenorm;
+  __shared__ float gsum[kWarps][32 * NV];
   const int lane = threadIdx.x & 31;
-  const int pad = (E + 7) / 8 * 8;
-  float* acc = reinterpret_cast<float*>(gsum4) + (threadIdx.x >> 5) * pad;
+  float* acc = gsum[threadIdx.x >> 5];
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= tokens) return;
   const T* row = logits + (int64_t)t * E;
   T* grow = grad_logits + (int64_t)t * E;
-  const bool vec = E % kVec == 0;
   const int ks = k + shared;
   int e = -1;
   float gw = 0.f, l = 0.f;
@@ -413,57 +448,35 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
     gw = scale * grad_w[(int64_t)t * ks + lane];
   }
   const bool live = e >= 0 && e < E;
+  float p[kEvery ? NV : 1];
+  if constexpr (kEvery) {
+#pragma unroll
+    for (int v = 0; v < NV; v += kW) {
+      const int i = (32 * (v / kW) + lane) * kW;
+      if constexpr (kW == 1) {
+        p[v] = i < E ? load_logit(row + i) : -INFINITY;
+      } else {
+        float q[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (i < E) load4(row + i, q);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) p[v + b] = q[b];
+      }
+    }
+  }
   if (live) l = load_logit(row + e);
   else gw = 0.f;
-  for (int i = 4 * lane; i < pad; i += 128) *reinterpret_cast<float4*>(acc + i) = make_float4(0.f, 0.f, 0.f, 0.f);
-  // kVec elements of the row
-  auto load = [&](int i, float (&v)[kVec]) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 q = __ldg(reinterpret_cast<const float4*>(row + i));
-      v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-    } else {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + i));
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        v[2 * b] = __uint_as_float(w[b] << 16);
-        v[2 * b + 1] = __uint_as_float(w[b] & 0xFFFF0000u);
-      }
-    }
-  };
-  auto store = [&](int i, const float (&v)[kVec]) {
-    if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(grow + i) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * b], v[2 * b + 1]);
-        w[b] = *reinterpret_cast<const uint32_t*>(&p);
-      }
-      *reinterpret_cast<uint4*>(grow + i) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  };
+  for (int i = 0; i < NV; i += 4)
+    *reinterpret_cast<float4*>(acc + 32 * i + 4 * lane) = make_float4(0.f, 0.f, 0.f, 0.f);
   float top = -INFINITY, z = 0.f, d;   // d: what slot `lane` adds to its expert
   if constexpr (kEvery) {
-    if (vec) {
-      for (int i = lane * kVec; i < E; i += 32 * kVec) {
-        float v[kVec];
-        load(i, v);
 #pragma unroll
-        for (int b = 0; b < kVec; ++b) top = fmaxf(top, v[b]);
-      }
-      top = warp_max(top);
-      for (int i = lane * kVec; i < E; i += 32 * kVec) {
-        float v[kVec];
-        load(i, v);
+    for (int v = 0; v < NV; ++v) top = fmaxf(top, p[v]);
+    top = warp_max(top);
 #pragma unroll
-        for (int b = 0; b < kVec; ++b) z += expf(v[b] - top);
-      }
-    } else {
-      for (int i = lane; i < E; i += 32) top = fmaxf(top, load_logit(row + i));
-      top = warp_max(top);
-      for (int i = lane; i < E; i += 32) z += expf(load_logit(row + i) - top);
+    for (int v = 0; v < NV; ++v) {
+      p[v] = p[v] == -INFINITY ? 0.f : expf(p[v] - top);
+      z += p[v];
     }
     z = warp_sum(z);
     d = gw;
@@ -490,25 +503,25 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
     }
   }
   __syncwarp();
-  const float dot = kEvery ? warp_sum(live ? gw * (expf(l - top) / z) : 0.f) : 0.f;
-  if (vec) {
-    for (int i = lane * kVec; i < E; i += 32 * kVec) {
-      float v[kVec], r[kVec];
-      if constexpr (kEvery) load(i, v);
+  const float inv = kEvery ? 1.f / z : 0.f;
+  const float dot = kEvery ? warp_sum(live ? gw * (expf(l - top) * inv) : 0.f) : 0.f;
 #pragma unroll
-      for (int b = 0; b < kVec; b += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(acc + i + b);
-        r[b] = a.x; r[b + 1] = a.y; r[b + 2] = a.z; r[b + 3] = a.w;
-      }
+  for (int v = 0; v < NV; v += kW) {
+    const int i = (32 * (v / kW) + lane) * kW;
+    if (i >= E) break;
+    if constexpr (kW == 1) {
+      float r = acc[i];
+      if constexpr (kEvery) r = p[v] * inv * (r - dot);
+      store_grad(grow + i, r);
+    } else {
+      const float4 a = *reinterpret_cast<const float4*>(acc + i);
+      float r[4] = {a.x, a.y, a.z, a.w};
       if constexpr (kEvery) {
 #pragma unroll
-        for (int b = 0; b < kVec; ++b) r[b] = expf(v[b] - top) / z * (r[b] - dot);
+        for (int b = 0; b < 4; ++b) r[b] = p[v + b] * inv * (r[b] - dot);
       }
-      store(i, r);
+      store4(grow + i, r);
     }
-  } else {
-    for (int i = lane; i < E; i += 32)
-      store_grad(grow + i, kEvery ? expf(load_logit(row + i) - top) / z * (acc[i] - dot) : acc[i]);
   }
 }
 
@@ -541,16 +554,24 @@ cudaError_t launch_gate_backward(const moe_shape& s, const moe_gate_desc& g, con
                                  const float* grad_w, void* grad_logits, cudaStream_t stream) {
   const int T = (int)s.T, E = (int)s.E, k = (int)s.topk, shared = (s.flags & MOE_FLAG_SHARED_EXPERT) ? 1 : 0;
   const dim3 grid((T + kWarps - 1) / kWarps);
-  const size_t smem = (size_t)kWarps * ((E + 7) / 8 * 8) * sizeof(float);
   auto go = [&](auto kernel, auto* l, auto* d) {
-    kernel<<<grid, kWarps * 32, smem, stream>>>(l, idx, grad_w, T, E, k, shared, g.scale, d);
+    kernel<<<grid, kWarps * 32, 0, stream>>>(l, idx, grad_w, T, E, k, shared, g.scale, d);
     return cudaGetLastError();
   };
-  auto by_form = [&](auto* l, auto* d) {
+  auto by_size = [&](auto* l, auto* d, auto sig, auto ren) {
     using L = std::remove_pointer_t<decltype(d)>;
-    if (g.score == MOE_SCORE_SIGMOID)
-      return s.renorm ? go(gate_backward_kernel<L, true, true>, l, d) : go(gate_backward_kernel<L, true, false>, l, d);
-    return s.renorm ? go(gate_backward_kernel<L, false, true>, l, d) : go(gate_backward_kernel<L, false, false>, l, d);
+    constexpr bool kSig = decltype(sig)::value, kRen = decltype(ren)::value;
+    if (E % 4) return go(gate_backward_kernel<L, kSig, kRen, 32, 1>, l, d);
+    if (E <= 128) return go(gate_backward_kernel<L, kSig, kRen, 4, 4>, l, d);
+    if (E <= 256) return go(gate_backward_kernel<L, kSig, kRen, 8, 4>, l, d);
+    if (E <= 512) return go(gate_backward_kernel<L, kSig, kRen, 16, 4>, l, d);
+    return go(gate_backward_kernel<L, kSig, kRen, 32, 4>, l, d);
+  };
+  auto by_form = [&](auto* l, auto* d) {
+    std::true_type yes;
+    std::false_type no;
+    if (g.score == MOE_SCORE_SIGMOID) return s.renorm ? by_size(l, d, yes, yes) : by_size(l, d, yes, no);
+    return s.renorm ? by_size(l, d, no, yes) : by_size(l, d, no, no);
   };
   return g.logits_dtype == MOE_BF16 ? by_form((const __nv_bfloat16*)logits, (__nv_bfloat16*)grad_logits)
                                     : by_form((const float*)logits, (float*)grad_logits);

@@ -1,6 +1,6 @@
-// Rows to int8 with one scale each: scale = max |x| / 127, q = x / scale
-// rounded to nearest even. Both divisions are correctly rounded ones, so that
-// the result is defined to the bit.
+// Rows to int8 with one scale each: scale = max |x| * (1 / 127), q = x / scale
+// rounded to nearest even. The reciprocal, the product and the quotient are
+// correctly rounded ones, so that the result is defined to the bit.
 //
 // One block per row (of all rows, or of the filled rows of windows).
 #include "moe_internal.cuh"
@@ -34,7 +34,7 @@ quant_i8_kernel(const T* __restrict__ x, int64_t rows, int cols, RowWindows win,
     for (int i = 0; i < kThreads / 32; ++i) m = max(m, part[i]);
     __syncthreads();
     const bool bad = m >= 0x7F800000u;
-    const float s = bad ? __int_as_float(0x7fc00000) : (m == 0 ? 1.f : fmaxf(__fdiv_rn(__uint_as_float(m), 127.f), 0x1p-126f));
+    const float s = bad ? __int_as_float(0x7fc00000) : (m == 0 ? 1.f : fmaxf(__fmul_rn(__uint_as_float(m), 1.f / 127.f), 0x1p-126f));
     if (threadIdx.x == 0) scale[row0 + r] = s;
     for (int i = threadIdx.x; i < cols; i += kThreads)
       q[(row0 + r) * cols + i] = bad ? 0 : (int8_t)__float2int_rn(__fdiv_rn(load_x(xr + i), s));

@@ -500,9 +500,10 @@ MOE_API moe_status moe_gate_backward(const moe_shape* shape, const moe_gate_desc
 
 /*
  * Rows to int8 with one scale each:
- *   scale[r] = max_k |x[r, k]| / 127 (at least 2^-126; 1 for a row of zeros)
+ *   scale[r] = max_k |x[r, k]| * (1 / 127) (at least 2^-126; 1 for a row of zeros)
  *   q[r, k]  = x[r, k] / scale[r], rounded to nearest, ties to even
- * both divisions correctly rounded in binary32, so q is the same everywhere.
+ * the reciprocal, the product and the quotient correctly rounded in binary32,
+ * so q is the same everywhere.
  *   rows, cols  >= 0; cols a multiple of 16, at most 2^24
  *   src_dtype   MOE_F32 or MOE_BF16
  *   x           [rows, cols] src_dtype, device

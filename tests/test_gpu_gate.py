@@ -151,6 +151,34 @@ def test_choice_at_a_border_binary32_cannot_see(dtype):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("near", [2, 9, 20, 31, 32, 33, 100])
+def test_few_candidates_at_a_border(score, near):
+    """`near` experts within 2^-24 of one another around the last slot, the
+    others clearly above (three) or below."""
+    c = Case(48, E=256, k=8, score=score, bias=True, renorm=0)
+    logits = c.logits(near)
+    logits[:] = logits[0]
+    s = torch.sigmoid(logits[0].double()) if score == "sigmoid" else torch.softmax(logits[0].double(), 0)
+    gen = torch.Generator().manual_seed(near)
+    order = torch.randperm(256, generator=gen)
+    target = torch.full((256,), 0.25, dtype=torch.float64)
+    target[order[:3]] = torch.tensor([1.5, 1.25, 1.125], dtype=torch.float64)
+    target[order[3:3 + near]] = 0.75
+    bias = (target.cuda() - s).float()
+    # the same bits in another order of rows: each row moves one logit by a unit
+    for t in range(48):
+        logits[t, order[3 + t % near]] *= 1 + 2.0 ** -23
+    check(c, logits, bias)
+    # and on the logits themselves: neighbouring binary32 numbers
+    c = Case(48, E=256, k=8, score=score)
+    l = torch.full((48, 256), -1.0)
+    l[:, order[:3]] = 2.0
+    steps = torch.randint(0, 8, (48, near), generator=gen).float()
+    l[:, order[3:3 + near]] = 1 + steps * 2.0 ** -23
+    check(c, l.cuda())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias", [False, True])
 def test_equal_candidates_go_to_the_lowest_index(score, bias):
     c = Case(5, E=96, k=8, score=score, bias=bias, groups=4, topk_groups=2, best=2)

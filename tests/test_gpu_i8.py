@@ -38,7 +38,7 @@ def quant_ref(x):
     amax = np.abs(x).max(1) if x.shape[1] else np.zeros(x.shape[0])
     bad = ~np.isfinite(x).all(1)
     with np.errstate(all="ignore"):
-        s = np.maximum((amax / 127).astype(np.float32), np.float32(2.0 ** -126))
+        s = np.maximum(amax.astype(np.float32) * (np.float32(1) / np.float32(127)), np.float32(2.0 ** -126))
         s = np.where(amax == 0, np.float32(1), s)
         q = np.rint((x / s.astype(np.float64)[:, None]).astype(np.float32))
     q[bad] = 0
