@@ -2,12 +2,12 @@
 // groups, top-k and renormalised, scaled weights; and its gradient.
 //
 // gate_kernel gives one warp a token. Lane i holds `per` = ceil(E / 32)
-// consecutive experts from i * per on, so that lower lanes hold lower experts
-// and, for most groupings, a group is a whole power-of-two set of lanes. Each lane
-// sorts 32-bit keys that order like its choice values c, the low bits given
-// to the place in the lane (a sorting network of min and max, two
-// instructions a comparison), and each of the topk rounds takes the largest
-// head with one warp reduction and pops it.
+// consecutive experts from i * per on, so that for most groupings a group is a
+// whole power-of-two set of lanes. Each lane sorts 32-bit keys that order like
+// its choice values c, their low 7 to 10 bits given to the expert (a sorting
+// network of min and max, two instructions a comparison), and each of the topk
+// rounds takes the largest head with one warp reduction, which names the
+// expert too, and pops it.
 //
 // What is chosen has to be what binary64 chooses. The keys drop low bits and
 // c = s + bias carries binary32 roundings, so the chosen values (and the best
@@ -20,6 +20,7 @@
 // The row is read once, four elements at a time where its alignment allows.
 // gate_backward_kernel also gives one warp a token, adds the chosen experts'
 // derivatives into a row of shared memory in slot order and writes the row.
+#include <algorithm>
 #include <type_traits>
 
 #include "moe_internal.cuh"
@@ -167,17 +168,52 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
   return sel;
 }
 
-// NV slots of a lane, the first `per` of them used; kBits of the key hold the slot.
+// Odd-even merge sort of key[kLo .. kLo + kN), largest first.
+template <int kLo, int kN, int kStep, int NV>
+__device__ __forceinline__ void merge_descending(uint32_t (&key)[NV]) {
+  if constexpr (2 * kStep < kN) {
+    merge_descending<kLo, kN, 2 * kStep>(key);
+    merge_descending<kLo + kStep, kN, 2 * kStep>(key);
+  }
+#pragma unroll
+  for (int i = 2 * kStep < kN ? kLo + kStep : kLo; i + kStep < kLo + kN; i += 2 * kStep) {
+    const uint32_t a = key[i], b = key[i + kStep];
+    key[i] = max(a, b);
+    key[i + kStep] = min(a, b);
+  }
+}
+template <int kLo, int kN, int NV>
+__device__ __forceinline__ void sort_descending(uint32_t (&key)[NV]) {
+  if constexpr (kN > 1) {
+    sort_descending<kLo, kN / 2>(key);
+    sort_descending<kLo + kN / 2, kN / 2>(key);
+    merge_descending<kLo, kN, 1>(key);
+  }
+}
+
+// What the kernel needs of a grouping.
+struct Groups {
+  int n;      // experts of a group
+  int span;   // lanes of a group, a power of two, or 0: groups are not sets of lanes
+};
+
+// s of one logit for the choice, within err0 (below) of its value.
+template <bool kSigmoid>
+__device__ __forceinline__ float quick_score(float l, float top, float inv_z) {
+  return kSigmoid ? __fdividef(1.f, 1.f + __expf(-l)) : __expf(l - top) * inv_z;
+}
+
+// NV slots of a lane, the first `per` of them used.
 template <typename T, bool kSigmoid, int NV>
 __global__ void __launch_bounds__(kWarps * 32)
 gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int tokens, int E, int per, int k,
-            int shared, int renorm, moe_gate_desc g, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
-            Header* hdr) {
-  constexpr int kBits = NV <= 4 ? 2 : NV <= 8 ? 3 : NV <= 16 ? 4 : 5;
-  constexpr uint32_t kSlot = (1u << kBits) - 1u;
+            int shared, int renorm, moe_gate_desc g, Groups gr, int32_t* __restrict__ topk_idx,
+            float* __restrict__ topk_w, Header* hdr) {
+  constexpr int kBits = NV <= 4 ? 7 : NV <= 8 ? 8 : NV <= 16 ? 9 : 10;   // 32 NV experts at most
+  constexpr uint32_t kIdx = (1u << kBits) - 1u;
   extern __shared__ double smem[];
   const int lane = threadIdx.x & 31;
-  double* scratch = smem + (threadIdx.x >> 5) * E;
+  double* scratch = smem + (threadIdx.x >> 5) * max(E, 16);
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= tokens) return;
   const T* row = logits + (int64_t)t * E;
@@ -189,7 +225,8 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
 
   float l[NV], c[NV];   // logits, choice values
   // wide loads where every lane's part starts on a boundary and none is cut
-  if (per == NV && E == 32 * NV) {
+  const bool wide = E == 32 * NV;
+  if (wide) {
 #pragma unroll
     for (int v = 0; v < NV; v += 4) {
       float q[4];
@@ -201,50 +238,27 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
 #pragma unroll
     for (int v = 0; v < NV; ++v) l[v] = v < mine ? load_logit(row + e0 + v) : 0.f;
   }
-  bool bad = false;
-  float top = -INFINITY;
+  if (bias) {   // c holds the bias until the scores are there
+    if (wide) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    bad |= !isfinite(l[v]);
-    if (v < mine) top = fmaxf(top, l[v]);
-  }
-  const bool lossless = sizeof(T) == 2 && !bias;   // the keys tell all choice values apart
-  const bool scores = bias || (g.groups > 1 && g.group_best == 2);
-  float z = 1.f;
-  if (!kSigmoid) {
-    top = warp_max(top);
-    if (scores || !renorm) {
-      float part = 0.f;
+      for (int v = 0; v < NV; v += 4) {
+        float q[4];
+        load4(bias + e0 + v, q);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) part += v < mine ? expf(l[v] - top) : 0.f;
-      z = warp_sum(part);
-    }
-  }
-  // err0 + err1 |c|: bound of the difference between c (of one or of the sum of
-  // a few) and its binary64 value. Sigmoid: exp 2^-22, the sum and the
-  // quotient 2^-24 each, all at most 3 * 2^-24 of s <= 1, and the bias's sum
-  // 2^-24 |c|. Softmax: exp's argument and value, and a sum of E terms in a
-  // tree of depth <= 37: below 2^-18 of the largest score 1 / z.
-  const float err0 = bias || scores ? (kSigmoid ? 0x1p-21f : 0x1p-18f / z) : 0.f;
-  const float err1 = bias ? 0x1p-22f : 0.f;
-  bool unsure = false;
-  if (scores) {
+        for (int b = 0; b < 4; ++b) c[v + b] = q[b];
+      }
+    } else {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) c[v] = kSigmoid ? 1.f / (1.f + expf(-l[v])) : expf(l[v] - top) / z;
-    if (bias) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (v < mine) {
-          const float b = __ldg(bias + e0 + v);
-          bad |= !isfinite(b);
-          c[v] += b;
-        }
+      for (int v = 0; v < NV; ++v) c[v] = v < mine ? __ldg(bias + e0 + v) : 0.f;
     }
   } else {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) c[v] = l[v];
+    for (int v = 0; v < NV; ++v) c[v] = 0.f;
   }
-  if (__any_sync(kFull, bad)) {
+  float zero = 0.f;   // stays 0 unless a value is not finite
+#pragma unroll
+  for (int v = 0; v < NV; ++v) zero = __fmaf_rn(l[v], 0.f, __fmaf_rn(c[v], 0.f, zero));
+  if (__any_sync(kFull, zero != 0.f)) {
     if (lane < ks) {
       idx[lane] = lane < k ? lane : E;
       out[lane] = lane < k ? __int_as_float(0x7fc00000) : 1.f;
@@ -252,134 +266,161 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     if (lane == 0) latch_error(hdr, MOE_ERR_NONFINITE, (uint32_t)t);
     return;
   }
+  const bool lossless = sizeof(T) == 2 && !bias;   // the keys tell all choice values apart
+  const bool scores = bias || (g.groups > 1 && g.group_best == 2);
+  float top = 0.f, z = 1.f, inv_z = 1.f;
+  if (!kSigmoid) {
+    top = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (v < mine) top = fmaxf(top, l[v]);
+    top = warp_max(top);
+    if (scores || !renorm) {
+      float part = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) part += v < mine ? __expf(l[v] - top) : 0.f;
+      z = warp_sum(part);
+      inv_z = 1.f / z;
+    }
+  }
+  // err0 + err1 |c|: how far c can be from its binary64 value, with exp off by
+  // (2 + 1.173 |x|) 2^-23 relative and the fast quotient by 2^-22.
+  // Sigmoid: s (1 - s) times the former is below 2^-23, the sum adds 2^-24, the
+  // quotient 2^-22. Softmax: x is itself off by |x| 2^-24; over z the errors of
+  // exp average to at most 10.5 * 2^-23 (of 1024 terms), and the sum has a
+  // depth of at most 37: below 2^-17 of the largest score 1 / z in all. The
+  // sum with the bias: 2^-24 |c|.
+  const float err0 = scores ? (kSigmoid ? 0x1p-21f : 0x1p-17f * inv_z) : 0.f;
+  const float err1 = bias ? 0x1p-23f : 0.f;
+  if (scores) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) c[v] += quick_score<kSigmoid>(l[v], top, inv_z);
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) c[v] = l[v];
+  }
 
-  // groups: `closed` has bit v where slot v's group is not open
-  uint32_t closed = 0;
+  // groups: which slots' groups are open, one bit each
+  uint32_t open = ~0u;
+  bool unsure = false;
   if (g.groups > 1) {
-    const int n = E / g.groups;
     float b1 = -INFINITY, b2 = -INFINITY;
     auto take = [&](float v) {
       b2 = fmaxf(b2, fminf(b1, v));
       b1 = fmaxf(b1, v);
     };
-    const int span = n / per;   // lanes of a group
-    const bool lanes = span * per == n && (span & (span - 1)) == 0;
-    if (lanes) {   // a group is an aligned set of lanes (and all of them are full)
+    int gi = lane;   // this lane's group
+    if (gr.span) {   // a group is an aligned set of lanes, all of them full
+      gi = lane >> (__ffs(gr.span) - 1);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (v < mine) take(c[v]);
-      for (int off = 1; off < span; off <<= 1) {
+      for (int off = 1; off < gr.span; off <<= 1) {
         const float o1 = __shfl_xor_sync(kFull, b1, off), o2 = __shfl_xor_sync(kFull, b2, off);
         b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
         b1 = fmaxf(b1, o1);
       }
-    } else {       // any other grouping: lane i looks at group i
+    } else {         // any other grouping: lane i looks at group i
       float* row_c = reinterpret_cast<float*>(scratch);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (v < mine) row_c[e0 + v] = c[v];
       __syncwarp();
       if (lane < g.groups)
-        for (int i = 0; i < n; ++i) take(row_c[lane * n + i]);
+        for (int i = 0; i < gr.n; ++i) take(row_c[lane * gr.n + i]);
       __syncwarp();
     }
     const bool two = g.group_best == 2;
     const float r = two ? b1 + b2 : b1;
     const float e = two ? 2.f * err0 + err1 * (fabsf(b1) + fabsf(b2)) + 0x1p-23f * fabsf(r)
-                        : err0 + err1 * fabsf(b1);
+                        : (scores ? err0 + err1 * fabsf(b1) : 0.f);
     const float lo = r - e, hi = r + e;
-    // lane i: whether its group (lanes: the one it belongs to) is open: fewer
-    // than topk_groups others may be above it
-    const int gi = lanes ? lane / span : lane;
+    // a group is open if fewer than topk_groups others may be above it
+    const int step = gr.span ? gr.span : 1;
     int above = 0, may = 0;
-    for (int h = 0; h < g.groups; ++h) {
-      const int src = lanes ? h * span : h;
-      const float olo = __shfl_sync(kFull, lo, src), ohi = __shfl_sync(kFull, hi, src);
-      if (e == 0.f) {   // exact: ties to the lowest group
-        above += olo > r || (olo == r && h < gi);
-        may = above;
-      } else if (h != gi) {
-        above += olo > hi;
-        may += !(ohi < lo);
+    if (scores) {
+      for (int h = 0; h < g.groups; ++h) {
+        const float olo = __shfl_sync(kFull, lo, h * step), ohi = __shfl_sync(kFull, hi, h * step);
+        above += olo > hi;       // not of itself
+        may += !(ohi < lo);      // of itself too
       }
+      --may;
+    } else {   // exact: ties to the lowest group
+      for (int h = 0; h < g.groups; ++h) {
+        const float o = __shfl_sync(kFull, r, h * step);
+        above += o > r || (o == r && h < gi);
+      }
+      may = above;
     }
-    const bool open = may < g.topk_groups;
-    unsure = gi < g.groups && !open && above < g.topk_groups;
-    const uint32_t opens = __ballot_sync(kFull, gi < g.groups && open);
+    const bool in = gi < g.groups;
+    unsure = in && may >= g.topk_groups && above < g.topk_groups;
+    const uint32_t opens = __ballot_sync(kFull, in && may < g.topk_groups);
+    if (gr.span) {
+      open = may < g.topk_groups ? ~0u : 0u;
+    } else {
+      open = 0;
+      int q = e0 / gr.n, at = e0 - q * gr.n;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int src = lanes ? lane : (e0 + v < E ? (e0 + v) / n : 0);
-      if (!((opens >> src) & 1u)) closed |= 1u << v;
+      for (int v = 0; v < NV; ++v) {
+        if (v < mine) open |= ((opens >> q) & 1u) << v;
+        if (++at == gr.n) { at = 0; ++q; }
+      }
     }
     if (!bias && scores) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) c[v] = l[v];   // the groups' scores only ranked the groups
+      for (int v = 0; v < NV; ++v) c[v] = l[v];   // the scores only ranked the groups
     }
   }
 
   uint32_t key[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
-    key[v] = v < mine && !((closed >> v) & 1u) ? (order_key(c[v]) & ~kSlot) | (kSlot - v) : kNoKey;
-  // odd-even merge sort, descending
-#pragma unroll
-  for (int p = 1; p < NV; p *= 2)
-#pragma unroll
-    for (int q = p; q >= 1; q /= 2)
-#pragma unroll
-      for (int j = q % p; j + q < NV; j += 2 * q)
-#pragma unroll
-        for (int i = 0; i < q; ++i)
-          if (j + i + q < NV && (j + i) / (2 * p) == (j + i + q) / (2 * p)) {
-            const uint32_t a = key[j + i], b = key[j + i + q];
-            key[j + i] = max(a, b);
-            key[j + i + q] = min(a, b);
-          }
-  int sel = -1;   // lane j: slot j's expert (lane k: the best one left, or -1)
-  auto pop = [&](int j) -> uint32_t {   // the largest head, into lane j
-    const uint32_t head = key[0] & ~kSlot;
-    const uint32_t m = __reduce_max_sync(kFull, head);
-    const int who = __ffs(__ballot_sync(kFull, head == m)) - 1;   // lowest lane: lowest expert
-    const int e = __shfl_sync(kFull, e0 + (int)(kSlot - (key[0] & kSlot)), who);
-    if (lane == j && m != kNoKey) sel = e;
-    if (lane == who) {
+    key[v] = v < mine && ((open >> v) & 1u) ? (order_key(c[v]) & ~kIdx) | (kIdx - (uint32_t)(e0 + v)) : kNoKey;
+  sort_descending<0, NV>(key);
+  uint32_t won = kNoKey;   // lane j: slot j's key (lane k: that of the best one left)
+  auto pop = [&](int j) {   // the largest head, into lane j
+    const uint32_t m = __reduce_max_sync(kFull, key[0]);
+    if (lane == j) won = m;
+    if (key[0] == m) {
 #pragma unroll
       for (int v = 0; v + 1 < NV; ++v) key[v] = key[v + 1];
       key[NV - 1] = kNoKey;
     }
-    return m;
   };
   const int rounds = lossless ? k : min(k + 1, 32);
+#pragma unroll 1
   for (int j = 0; j < rounds; ++j) pop(j);
+  int sel = won == kNoKey ? -1 : (int)(kIdx - (won & kIdx));
+  float lj = sel >= 0 ? load_logit(row + sel) : 0.f;
   unsure = __any_sync(kFull, unsure);   // which groups are open
   if (!lossless && !unsure) {
-    float v = sel >= 0 ? load_logit(row + sel) : -INFINITY;
-    if (bias && sel >= 0) v = (kSigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / z) + __ldg(bias + sel);
+    float v = -INFINITY;
+    if (sel >= 0) v = bias ? __ldg(bias + sel) + quick_score<kSigmoid>(lj, top, inv_z) : lj;
     const float next = __shfl_down_sync(kFull, v, 1);
     const int nsel = __shfl_down_sync(kFull, sel, 1);
     const float mag = fmaxf(fmaxf(fabsf(v), sel >= 0 && nsel >= 0 ? fabsf(next) : 0.f), 0x1p-126f);
-    const float cut = ldexpf(mag, kBits - 23);   // what the keys drop
-    const float near = 2.f * (err0 + err1 * mag) + cut;
+    const float near = 2.f * (err0 + err1 * mag);       // between two choice values
+    const float cut = mag * (float)(1u << kBits) * 0x1p-23f;   // and what the keys drop
     bool doubt = false;   // between lanes j and j + 1
     if (lane + 1 < k) doubt = bias ? !(v - next > near) : !(v > next || (v == next && sel < nsel));
-    if (lane == k - 1) doubt = k == 32 || (nsel >= 0 && !(v - next > near));
+    if (lane == k - 1) doubt = k == 32 || (nsel >= 0 && !(v - next > near + cut));
     if (__any_sync(kFull, doubt)) {
       // pop whatever may reach the last slot
-      const uint32_t lim = order_key(__shfl_sync(kFull, v - near, k - 1));
+      const uint32_t lim = order_key(__shfl_sync(kFull, v - (near + cut), k - 1));
       int n = rounds;
       uint32_t m = __reduce_max_sync(kFull, key[0]);
-      while (n < 32 && m != kNoKey && (m | kSlot) >= lim) {
+      while (n < 32 && m != kNoKey && (m | kIdx) >= lim) {
         pop(n++);
         m = __reduce_max_sync(kFull, key[0]);
       }
-      unsure = m != kNoKey && (m | kSlot) >= lim;   // more than a warp of them
+      unsure = m != kNoKey && (m | kIdx) >= lim;   // more than a warp of them
       if (!unsure) {
+        sel = won == kNoKey ? -1 : (int)(kIdx - (won & kIdx));
         double zd = 1.0;
         if (!kSigmoid && bias) {
           double part = 0.0;
-#pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (i < mine) part += exp((double)l[i] - (double)top);
+#pragma unroll 1
+          for (int i = 0; i < mine; ++i) part += exp((double)load_logit(row + e0 + i) - (double)top);
           zd = warp_sum(part);
         }
         double c64 = -INFINITY;
@@ -403,13 +444,12 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     }
   }
   if (unsure) {
-    top = warp_max(top);
     __syncwarp();
     sel = choose_exactly<T, kSigmoid>(row, bias, E, k, g, top, scratch);
   }
 
   const bool live = lane < k;
-  const float lj = live ? load_logit(row + sel) : 0.f;
+  if (!lossless || unsure) lj = live ? load_logit(row + sel) : 0.f;
   float a;
   if (renorm) {
     a = renorm_term<kSigmoid>(lj, live);
@@ -531,9 +571,11 @@ cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits
                         float* w) {
   const int T = (int)c.s.T, E = (int)c.routed_E, k = (int)c.routed_k, per = (E + 31) / 32;
   const dim3 grid((T + kWarps - 1) / kWarps);
-  const size_t smem = (size_t)kWarps * E * sizeof(double);   // <= 32 KB
+  const size_t smem = (size_t)kWarps * std::max(E, 16) * sizeof(double);   // a warp: a row, or 32 slots; <= 32 KB
+  Groups gr{E / g.groups, 0};
+  if (gr.n % per == 0 && ((gr.n / per) & (gr.n / per - 1)) == 0) gr.span = gr.n / per;
   auto go = [&](auto kernel, auto* l) {
-    kernel<<<grid, kWarps * 32, smem, c.stream>>>(l, bias, T, E, per, k, c.shared, c.s.renorm, g, idx, w, c.ws.hdr);
+    kernel<<<grid, kWarps * 32, smem, c.stream>>>(l, bias, T, E, per, k, c.shared, c.s.renorm, g, gr, idx, w, c.ws.hdr);
     return cudaGetLastError();
   };
   auto by_size = [&](auto* l, auto sig) {
