@@ -1,25 +1,27 @@
 // The gate: routing with softmax or sigmoid scores, a balance bias, expert
 // groups, top-k and renormalised, scaled weights; and its gradient.
 //
-// gate_kernel gives one warp a token. Lane i holds `per` = ceil(E / 32)
-// consecutive experts from i * per on, so that for most groupings a group is a
-// whole power-of-two set of lanes. Each lane sorts 32-bit keys that order like
-// its choice values c, their low 7 to 10 bits given to the expert (a sorting
-// network of min and max, two instructions a comparison), and each of the topk
-// rounds takes the largest head with one warp reduction, which names the
-// expert too, and pops it.
+// gate_kernel gives a token a set of S lanes: a warp, or for many tokens a half
+// or a quarter of one, which shares the work that does not grow with E. Lane i
+// holds `per` = ceil(E / S) consecutive experts from i * per on, so that for
+// most groupings a group is a power-of-two set of lanes. Each lane sorts 32-bit
+// keys that order like its choice values c, their low 6 to 10 bits given to the
+// expert (a sorting network of min and max, two instructions a comparison), and
+// each of the topk rounds takes the largest head with one reduction, which
+// names the expert too, and pops it.
 //
 // What is chosen has to be what binary64 chooses. The keys drop low bits and
 // c = s + bias carries binary32 roundings, so the chosen values (and the best
-// one left) are compared once more with the bounds of both: a token with two
-// neighbours closer than that, or with a group at the border of the open ones
-// closer than that, is done over in binary64 (choose_exactly). Without a bias
-// c is the logit itself; bf16 logits then lose nothing in the keys and need no
-// second look.
+// one left) are compared once more with the bounds of both. Where two
+// neighbours are closer than that, every candidate that could still belong to
+// the topk is popped, one to a lane, and these are ordered in binary64; a token
+// with a group at the border of the open ones closer than that is done over in
+// binary64 (choose_exactly). Without a bias c is the logit itself; bf16 logits
+// then lose nothing in the keys and need no second look.
 //
-// The row is read once, four elements at a time where its alignment allows.
-// gate_backward_kernel also gives one warp a token, adds the chosen experts'
-// derivatives into a row of shared memory in slot order and writes the row.
+// gate_backward_kernel writes what every expert gets (zero, or -p_e dot for a
+// plain softmax) 16 bytes a lane, then the chosen experts' derivatives over it.
+// The row is read only for a plain softmax.
 #include <algorithm>
 #include <type_traits>
 
@@ -30,6 +32,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kManyTokens = 4096;   // from here on a token gets fewer lanes than a warp
 constexpr uint32_t kNoKey = 0u;   // below the key of every number
 
 // 32-bit key that orders like the number
@@ -62,28 +65,82 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
   v[2] = __uint_as_float(q.y << 16);
   v[3] = __uint_as_float(q.y & 0xFFFF0000u);
 }
-__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+template <int kW, typename T>
+__device__ __forceinline__ void load_vec(const T* p, float (&v)[kW]) {
+  if constexpr (kW == 1) {
+    v[0] = load_logit(p);
+  } else {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if constexpr (kW == 4) {
+        v[b] = __uint_as_float(w[b]);
+      } else {
+        v[2 * b] = __uint_as_float(w[b] << 16);
+        v[2 * b + 1] = __uint_as_float(w[b] & 0xFFFF0000u);
+      }
+    }
+  }
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+template <int kW, typename T>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[kW]) {
+  if constexpr (kW == 1) {
+    store_grad(p, v[0]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if constexpr (kW == 4) {
+        w[b] = __float_as_uint(v[b]);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * b], v[2 * b + 1]);
+        w[b] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Reductions over the S lanes of a token (all 32 lanes take part).
+template <int S, typename V>
+__device__ __forceinline__ V sub_sum(V v) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+  for (int off = S / 2; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int S>
+__device__ __forceinline__ float sub_max(float v) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+  for (int off = S / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
   return v;
 }
-__device__ __forceinline__ double warp_sum(double v) {
+template <int S>
+__device__ __forceinline__ uint32_t sub_max(uint32_t v) {
+  if constexpr (S == 32) return __reduce_max_sync(kFull, v);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+  for (int off = S / 2; off > 0; off >>= 1) v = max(v, __shfl_xor_sync(kFull, v, off));
   return v;
+}
+// Whether p holds in any of the token's lanes.
+template <int S>
+__device__ __forceinline__ bool sub_any(bool p) {
+  const uint32_t all = __ballot_sync(kFull, p);
+  if constexpr (S == 32) return all != 0u;
+  return ((all >> ((threadIdx.x & 31) / S * S)) & ((1u << (S & 31)) - 1u)) != 0u;
+}
+
+// exp for the choice: off by (2 + 1.173 |x|) 2^-23 relative at most
+__device__ __forceinline__ float quick_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+// 1 / x, x >= 1 (0 for infinity): off by 2^-22 relative at most
+__device__ __forceinline__ float quick_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // The warp's best (value, index): larger value, lower index on a tie.
@@ -101,9 +158,9 @@ __device__ __forceinline__ void warp_best(double& v, int& i) {
 // renormalised score. The factor keeps the largest term near 1, where the
 // scores themselves would underflow: exp(l - max) for softmax; for sigmoid,
 // with m = min(0, max l), exp(-m) s = exp(l - m) / (1 + exp(l)).
-template <bool kSigmoid>
+template <bool kSigmoid, int S>
 __device__ __forceinline__ float renorm_term(float l, bool live) {
-  const float top = warp_max(live ? l : -INFINITY);
+  const float top = sub_max<S>(live ? l : -INFINITY);
   if (!live) return 0.f;
   if (!kSigmoid) return expf(l - top);
   const float m = fminf(top, 0.f);
@@ -120,7 +177,7 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
   if (!kSigmoid) {
     z = 0.0;
     for (int e = lane; e < E; e += 32) z += exp((double)load_logit(row + e) - (double)top);
-    z = warp_sum(z);
+    z = sub_sum<32>(z);
   }
   auto score = [&](int e) -> double {
     const double l = load_logit(row + e);
@@ -195,37 +252,38 @@ __device__ __forceinline__ void sort_descending(uint32_t (&key)[NV]) {
 struct Groups {
   int n;      // experts of a group
   int span;   // lanes of a group, a power of two, or 0: groups are not sets of lanes
+  int scratch;   // doubles of shared memory a warp
 };
 
 // s of one logit for the choice, within err0 (below) of its value.
 template <bool kSigmoid>
 __device__ __forceinline__ float quick_score(float l, float top, float inv_z) {
-  return kSigmoid ? __fdividef(1.f, 1.f + __expf(-l)) : __expf(l - top) * inv_z;
+  return kSigmoid ? quick_rcp(1.f + quick_exp(-l)) : quick_exp(l - top) * inv_z;
 }
 
-// NV slots of a lane, the first `per` of them used.
-template <typename T, bool kSigmoid, int NV>
+// NV slots of a lane, the first `per` of them used; S lanes a token.
+template <typename T, bool kSigmoid, int NV, int S>
 __global__ void __launch_bounds__(kWarps * 32)
 gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int tokens, int E, int per, int k,
             int shared, int renorm, moe_gate_desc g, Groups gr, int32_t* __restrict__ topk_idx,
             float* __restrict__ topk_w, Header* hdr) {
-  constexpr int kBits = NV <= 4 ? 7 : NV <= 8 ? 8 : NV <= 16 ? 9 : 10;   // 32 NV experts at most
+  constexpr int kBits = NV * S <= 64 ? 6 : NV * S <= 128 ? 7 : NV * S <= 256 ? 8 : NV * S <= 512 ? 9 : 10;
   constexpr uint32_t kIdx = (1u << kBits) - 1u;
   extern __shared__ double smem[];
   const int lane = threadIdx.x & 31;
-  double* scratch = smem + (threadIdx.x >> 5) * max(E, 16);
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= tokens) return;
+  const int li = lane % S, base = lane - li;   // place among the token's lanes, and their first
+  double* scratch = smem + (threadIdx.x >> 5) * gr.scratch;
+  const int warp_t = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * (32 / S);
+  if (warp_t >= tokens) return;
+  const int t = min(warp_t + lane / S, tokens - 1);   // lanes past the last token do it once more
+  const bool mine_to_store = warp_t + lane / S < tokens;
   const T* row = logits + (int64_t)t * E;
-  const int ks = k + shared;
-  int32_t* idx = topk_idx + (int64_t)t * ks;
-  float* out = topk_w + (int64_t)t * ks;
-  const int e0 = lane * per;
+  const int e0 = li * per;
   const int mine = max(0, min(per, E - e0));   // experts of this lane
 
   float l[NV], c[NV];   // logits, choice values
   // wide loads where every lane's part starts on a boundary and none is cut
-  const bool wide = E == 32 * NV;
+  const bool wide = E == S * NV;
   if (wide) {
 #pragma unroll
     for (int v = 0; v < NV; v += 4) {
@@ -258,30 +316,26 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
   float zero = 0.f;   // stays 0 unless a value is not finite
 #pragma unroll
   for (int v = 0; v < NV; ++v) zero = __fmaf_rn(l[v], 0.f, __fmaf_rn(c[v], 0.f, zero));
-  if (__any_sync(kFull, zero != 0.f)) {
-    if (lane < ks) {
-      idx[lane] = lane < k ? lane : E;
-      out[lane] = lane < k ? __int_as_float(0x7fc00000) : 1.f;
-    }
-    if (lane == 0) latch_error(hdr, MOE_ERR_NONFINITE, (uint32_t)t);
-    return;
+  const bool dead = sub_any<S>(zero != 0.f);
+  if (dead) {   // goes along as a row of zeros
+#pragma unroll
+    for (int v = 0; v < NV; ++v) l[v] = c[v] = 0.f;
+    if (li == 0 && mine_to_store) latch_error(hdr, MOE_ERR_NONFINITE, (uint32_t)t);
   }
   const bool lossless = sizeof(T) == 2 && !bias;   // the keys tell all choice values apart
   const bool scores = bias || (g.groups > 1 && g.group_best == 2);
   float top = 0.f, z = 1.f, inv_z = 1.f;
-  if (!kSigmoid) {
+  if (!kSigmoid && (scores || !renorm)) {
     top = -INFINITY;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
       if (v < mine) top = fmaxf(top, l[v]);
-    top = warp_max(top);
-    if (scores || !renorm) {
-      float part = 0.f;
+    top = sub_max<S>(top);
+    float part = 0.f;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) part += v < mine ? __expf(l[v] - top) : 0.f;
-      z = warp_sum(part);
-      inv_z = 1.f / z;
-    }
+    for (int v = 0; v < NV; ++v) part += v < mine ? quick_exp(l[v] - top) : 0.f;
+    z = sub_sum<S>(part);
+    inv_z = 1.f / z;
   }
   // err0 + err1 |c|: how far c can be from its binary64 value, with exp off by
   // (2 + 1.173 |x|) 2^-23 relative and the fast quotient by 2^-22.
@@ -309,9 +363,9 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
       b2 = fmaxf(b2, fminf(b1, v));
       b1 = fmaxf(b1, v);
     };
-    int gi = lane;   // this lane's group
+    int gi = li;   // this lane's group
     if (gr.span) {   // a group is an aligned set of lanes, all of them full
-      gi = lane >> (__ffs(gr.span) - 1);
+      gi = li >> (__ffs(gr.span) - 1);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (v < mine) take(c[v]);
@@ -321,13 +375,13 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
         b1 = fmaxf(b1, o1);
       }
     } else {         // any other grouping: lane i looks at group i
-      float* row_c = reinterpret_cast<float*>(scratch);
+      float* row_c = reinterpret_cast<float*>(scratch) + lane / S * E;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (v < mine) row_c[e0 + v] = c[v];
       __syncwarp();
-      if (lane < g.groups)
-        for (int i = 0; i < gr.n; ++i) take(row_c[lane * gr.n + i]);
+      if (li < g.groups)
+        for (int i = 0; i < gr.n; ++i) take(row_c[li * gr.n + i]);
       __syncwarp();
     }
     const bool two = g.group_best == 2;
@@ -340,21 +394,21 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     int above = 0, may = 0;
     if (scores) {
       for (int h = 0; h < g.groups; ++h) {
-        const float olo = __shfl_sync(kFull, lo, h * step), ohi = __shfl_sync(kFull, hi, h * step);
+        const float olo = __shfl_sync(kFull, lo, base + h * step), ohi = __shfl_sync(kFull, hi, base + h * step);
         above += olo > hi;       // not of itself
         may += !(ohi < lo);      // of itself too
       }
       --may;
     } else {   // exact: ties to the lowest group
       for (int h = 0; h < g.groups; ++h) {
-        const float o = __shfl_sync(kFull, r, h * step);
+        const float o = __shfl_sync(kFull, r, base + h * step);
         above += o > r || (o == r && h < gi);
       }
       may = above;
     }
     const bool in = gi < g.groups;
     unsure = in && may >= g.topk_groups && above < g.topk_groups;
-    const uint32_t opens = __ballot_sync(kFull, in && may < g.topk_groups);
+    const uint32_t opens = __ballot_sync(kFull, in && may < g.topk_groups) >> base;
     if (gr.span) {
       open = may < g.topk_groups ? ~0u : 0u;
     } else {
@@ -378,22 +432,21 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     key[v] = v < mine && ((open >> v) & 1u) ? (order_key(c[v]) & ~kIdx) | (kIdx - (uint32_t)(e0 + v)) : kNoKey;
   sort_descending<0, NV>(key);
   uint32_t won = kNoKey;   // lane j: slot j's key (lane k: that of the best one left)
-  auto pop = [&](int j) {   // the largest head, into lane j
-    const uint32_t m = __reduce_max_sync(kFull, key[0]);
-    if (lane == j) won = m;
+  auto pop = [&](uint32_t m, int j) {   // the largest head m, into lane j
+    if (li == j) won = m;
     if (key[0] == m) {
 #pragma unroll
       for (int v = 0; v + 1 < NV; ++v) key[v] = key[v + 1];
       key[NV - 1] = kNoKey;
     }
   };
-  const int rounds = lossless ? k : min(k + 1, 32);
+  const int rounds = lossless ? k : min(k + 1, S);
 #pragma unroll 1
-  for (int j = 0; j < rounds; ++j) pop(j);
+  for (int j = 0; j < rounds; ++j) pop(sub_max<S>(key[0]), j);
   int sel = won == kNoKey ? -1 : (int)(kIdx - (won & kIdx));
   float lj = sel >= 0 ? load_logit(row + sel) : 0.f;
-  unsure = __any_sync(kFull, unsure);   // which groups are open
-  if (!lossless && !unsure) {
+  unsure = sub_any<S>(unsure) && !dead;   // which groups are open
+  if (!lossless) {
     float v = -INFINITY;
     if (sel >= 0) v = bias ? __ldg(bias + sel) + quick_score<kSigmoid>(lj, top, inv_z) : lj;
     const float next = __shfl_down_sync(kFull, v, 1);
@@ -402,189 +455,206 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     const float near = 2.f * (err0 + err1 * mag);       // between two choice values
     const float cut = mag * (float)(1u << kBits) * 0x1p-23f;   // and what the keys drop
     bool doubt = false;   // between lanes j and j + 1
-    if (lane + 1 < k) doubt = bias ? !(v - next > near) : !(v > next || (v == next && sel < nsel));
-    if (lane == k - 1) doubt = k == 32 || (nsel >= 0 && !(v - next > near + cut));
+    if (li + 1 < k) doubt = bias ? !(v - next > near) : !(v > next || (v == next && sel < nsel));
+    if (li == k - 1) doubt = k == S || (nsel >= 0 && !(v - next > near + cut));
+    doubt = sub_any<S>(doubt) && !dead && !unsure;
     if (__any_sync(kFull, doubt)) {
       // pop whatever may reach the last slot
-      const uint32_t lim = order_key(__shfl_sync(kFull, v - (near + cut), k - 1));
+      const uint32_t lim = order_key(__shfl_sync(kFull, v - (near + cut), base + k - 1));
       int n = rounds;
-      uint32_t m = __reduce_max_sync(kFull, key[0]);
-      while (n < 32 && m != kNoKey && (m | kIdx) >= lim) {
-        pop(n++);
-        m = __reduce_max_sync(kFull, key[0]);
+      uint32_t m = sub_max<S>(key[0]);
+      auto reaches = [&]() { return doubt && m != kNoKey && (m | kIdx) >= lim; };
+      while (__any_sync(kFull, reaches() && n < S)) {
+        if (reaches() && n < S) pop(m, n++);
+        m = sub_max<S>(key[0]);
       }
-      unsure = m != kNoKey && (m | kIdx) >= lim;   // more than a warp of them
-      if (!unsure) {
-        sel = won == kNoKey ? -1 : (int)(kIdx - (won & kIdx));
-        double zd = 1.0;
-        if (!kSigmoid && bias) {
-          double part = 0.0;
+      unsure = unsure || reaches();   // more candidates than lanes
+      const int cand = won == kNoKey ? -1 : (int)(kIdx - (won & kIdx));
+      double zd = 1.0;
+      if (!kSigmoid && bias) {
+        double part = 0.0;
 #pragma unroll 1
-          for (int i = 0; i < mine; ++i) part += exp((double)load_logit(row + e0 + i) - (double)top);
-          zd = warp_sum(part);
-        }
-        double c64 = -INFINITY;
-        if (sel >= 0) {
-          const double x = load_logit(row + sel);
-          c64 = !bias ? x
-                      : (kSigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top) / zd) + (double)__ldg(bias + sel);
-        }
-        int rank = 0;
-        for (int i = 0; i < n; ++i) {
-          const double o = __shfl_sync(kFull, c64, i);
-          const int os = __shfl_sync(kFull, sel, i);
-          rank += o > c64 || (o == c64 && os < sel);
-        }
-        int* slots = reinterpret_cast<int*>(scratch);
-        __syncwarp();
-        if (sel >= 0 && rank < k) slots[rank] = sel;
-        __syncwarp();
-        if (lane < k) sel = slots[lane];
+        for (int i = 0; i < mine; ++i) part += exp((double)load_logit(row + e0 + i) - (double)top);
+        zd = sub_sum<S>(part);
       }
+      double c64 = -INFINITY;
+      if (cand >= 0) {
+        const double x = load_logit(row + cand);
+        c64 = !bias ? x
+                    : (kSigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top) / zd) + (double)__ldg(bias + cand);
+      }
+      int rank = 0;
+      for (int i = 0; i < S; ++i) {
+        const double o = __shfl_sync(kFull, c64, base + i);
+        const int os = __shfl_sync(kFull, cand, base + i);
+        rank += os >= 0 && (o > c64 || (o == c64 && os < cand));
+      }
+      int* slots = reinterpret_cast<int*>(scratch) + base;
+      __syncwarp();
+      if (doubt && cand >= 0 && rank < k) slots[rank] = cand;
+      __syncwarp();
+      if (doubt && !unsure && li < k) sel = slots[li];
     }
   }
-  if (unsure) {
+  uint32_t again = __ballot_sync(kFull, unsure);
+  while (again) {   // a token at a time, by the whole warp
+    const int src = __ffs(again) - 1, first = src - src % S;
+    again &= ~((S == 32 ? kFull : (1u << (S & 31)) - 1u) << first);
     __syncwarp();
-    sel = choose_exactly<T, kSigmoid>(row, bias, E, k, g, top, scratch);
+    const int s = choose_exactly<T, kSigmoid>(logits + (int64_t)__shfl_sync(kFull, t, first) * E, bias, E, k, g,
+                                              __shfl_sync(kFull, top, first), scratch);
+    const int got = __shfl_sync(kFull, s, li);
+    if (base == first && li < k) sel = got;
+    __syncwarp();
   }
 
-  const bool live = lane < k;
-  if (!lossless || unsure) lj = live ? load_logit(row + sel) : 0.f;
+  const bool live = li < k;
+  lj = live && sel >= 0 ? load_logit(row + sel) : 0.f;   // -1 in a dead row only
   float a;
   if (renorm) {
-    a = renorm_term<kSigmoid>(lj, live);
-    a /= warp_sum(a);
+    a = renorm_term<kSigmoid, S>(lj, live);
+    a /= sub_sum<S>(a);
   } else {
     a = kSigmoid ? 1.f / (1.f + expf(-lj)) : expf(lj - top) / z;
   }
-  if (lane < ks) {
-    idx[lane] = live ? sel : E;
-    out[lane] = live ? g.scale * a : 1.f;
+  const int ks = k + shared;
+  int32_t* idx = topk_idx + (int64_t)t * ks;
+  float* out = topk_w + (int64_t)t * ks;
+  if (mine_to_store && live) {
+    idx[li] = dead ? li : sel;
+    out[li] = dead ? __int_as_float(0x7fc00000) : g.scale * a;
+  }
+  if (mine_to_store && shared && li == 0) {
+    idx[k] = E;
+    out[k] = 1.f;
   }
 }
 
-// Lane i holds elements (32 c + i) kW .. + kW - 1 of the row, c < NV / kW:
-// kW = 4 where rows start on a boundary of four elements, else 1. The row is
-// read only for a softmax that is not renormalised, where every logit has a
-// gradient, and then once.
-template <typename T, bool kSigmoid, bool kRenorm, int NV, int kW>
+// S lanes a token (topk <= S). Elements go kW at a time, 16 bytes where rows
+// start on such a boundary, else one.
+template <typename T, bool kSigmoid, bool kRenorm, int S, int kW>
 __global__ void __launch_bounds__(kWarps * 32)
 gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ topk_idx,
                      const float* __restrict__ grad_w, int tokens, int E, int k, int shared, float scale,
                      T* __restrict__ grad_logits) {
   constexpr bool kEvery = !kSigmoid && !kRenorm;
-  __shared__ float gsum[kWarps][32 * NV];
-  const int lane = threadIdx.x & 31;
-  float* acc = gsum[threadIdx.x >> 5];
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= tokens) return;
+  const int lane = threadIdx.x & 31, li = lane % S, base = lane - li;
+  const int warp_t = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * (32 / S);
+  if (warp_t >= tokens) return;
+  const int t = min(warp_t + lane / S, tokens - 1);
+  const bool real = warp_t + lane / S < tokens;   // lanes past the last token store nothing
   const T* row = logits + (int64_t)t * E;
   T* grow = grad_logits + (int64_t)t * E;
   const int ks = k + shared;
   int e = -1;
   float gw = 0.f, l = 0.f;
-  if (lane < k) {
-    e = topk_idx[(int64_t)t * ks + lane];
-    gw = scale * grad_w[(int64_t)t * ks + lane];
+  if (li < k) {
+    e = topk_idx[(int64_t)t * ks + li];
+    gw = scale * grad_w[(int64_t)t * ks + li];
   }
   const bool live = e >= 0 && e < E;
-  float p[kEvery ? NV : 1];
-  if constexpr (kEvery) {
-#pragma unroll
-    for (int v = 0; v < NV; v += kW) {
-      const int i = (32 * (v / kW) + lane) * kW;
-      if constexpr (kW == 1) {
-        p[v] = i < E ? load_logit(row + i) : -INFINITY;
-      } else {
-        float q[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (i < E) load4(row + i, q);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) p[v + b] = q[b];
-      }
-    }
-  }
   if (live) l = load_logit(row + e);
   else gw = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; i += 4)
-    *reinterpret_cast<float4*>(acc + 32 * i + 4 * lane) = make_float4(0.f, 0.f, 0.f, 0.f);
-  float top = -INFINITY, z = 0.f, d;   // d: what slot `lane` adds to its expert
+  float top = 0.f, inv = 0.f, dot = 0.f;
   if constexpr (kEvery) {
+    // running maximum and sum in one pass
+    float m = -INFINITY, z = 0.f;
+    for (int i = li * kW; i < E; i += S * kW) {
+      float v[kW];
+      load_vec<kW>(row + i, v);
+      float vm = v[0];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) top = fmaxf(top, p[v]);
-    top = warp_max(top);
+      for (int b = 1; b < kW; ++b) vm = fmaxf(vm, v[b]);
+      if (vm > m) {
+        z *= __expf(m - vm);
+        m = vm;
+      }
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      p[v] = p[v] == -INFINITY ? 0.f : expf(p[v] - top);
-      z += p[v];
+      for (int b = 0; b < kW; ++b) z += v[b] == -INFINITY ? 0.f : __expf(v[b] - m);
     }
-    z = warp_sum(z);
+    top = sub_max<S>(m);
+    z = sub_sum<S>(z == 0.f ? 0.f : z * __expf(m - top));
+    inv = 1.f / z;
+    dot = sub_sum<S>(live ? gw * (expf(l - top) * inv) : 0.f);
+  }
+  // what every expert gets
+  if (real) {
+    for (int i = li * kW; i < E; i += S * kW) {
+      float v[kW];
+      if constexpr (kEvery) {
+        load_vec<kW>(row + i, v);
+#pragma unroll
+        for (int b = 0; b < kW; ++b) v[b] = __expf(v[b] - top) * inv * -dot;
+      } else {
+#pragma unroll
+        for (int b = 0; b < kW; ++b) v[b] = 0.f;
+      }
+      store_vec<kW>(grow + i, v);
+    }
+  }
+  // and what the chosen ones get: d from slot li
+  float d;
+  if constexpr (kEvery) {
     d = gw;
   } else {
-    float q = kRenorm ? renorm_term<kSigmoid>(l, live) : 1.f / (1.f + expf(-l));
+    float q = kRenorm ? renorm_term<kSigmoid, S>(l, live) : 1.f / (1.f + expf(-l));
     float gd = gw;
     if (kRenorm) {
-      const float s = warp_sum(q);
+      const float s = sub_sum<S>(q);
       q = s == 0.f ? 0.f : q / s;   // 0: no slot takes part
-      gd -= warp_sum(q * gw);
+      gd -= sub_sum<S>(q * gw);
     }
     d = q * gd;
     if (kSigmoid) d *= 1.f / (1.f + expf(l));
   }
-  __syncwarp();
-  // an expert named twice sums in slot order; nearly always none is
-  const uint32_t same = __match_any_sync(kFull, live ? e : ~lane);
-  if (!__any_sync(kFull, (same & (same - 1u)) != 0u)) {
-    if (live) acc[e] = d;
-  } else {
+  // an expert named twice: every slot of it writes their sum, in slot order
+  bool twice = false;
+#pragma unroll 1
+  for (int off = 1; off < S; ++off) {
+    const int o = __shfl_xor_sync(kFull, live ? e : -1, off);
+    twice |= live && o == e;
+  }
+  if (__any_sync(kFull, twice)) {
+    float sum = 0.f;
     for (int j = 0; j < k; ++j) {
-      if (lane == j && live) acc[e] += d;
-      __syncwarp();
+      const float dj = __shfl_sync(kFull, d, base + j);
+      const int ej = __shfl_sync(kFull, live ? e : -1, base + j);
+      if (ej == e) sum += dj;
     }
+    d = sum;
   }
-  __syncwarp();
-  const float inv = kEvery ? 1.f / z : 0.f;
-  const float dot = kEvery ? warp_sum(live ? gw * (expf(l - top) * inv) : 0.f) : 0.f;
-#pragma unroll
-  for (int v = 0; v < NV; v += kW) {
-    const int i = (32 * (v / kW) + lane) * kW;
-    if (i >= E) break;
-    if constexpr (kW == 1) {
-      float r = acc[i];
-      if constexpr (kEvery) r = p[v] * inv * (r - dot);
-      store_grad(grow + i, r);
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(acc + i);
-      float r[4] = {a.x, a.y, a.z, a.w};
-      if constexpr (kEvery) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b) r[b] = p[v + b] * inv * (r[b] - dot);
-      }
-      store4(grow + i, r);
-    }
-  }
+  if constexpr (kEvery) d = expf(l - top) * inv * (d - dot);
+  __syncwarp();   // after the stores above
+  if (real && live) store_grad(grow + e, d);
 }
 
 }  // namespace
 
 cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits, const float* bias, int32_t* idx,
                         float* w) {
-  const int T = (int)c.s.T, E = (int)c.routed_E, k = (int)c.routed_k, per = (E + 31) / 32;
-  const dim3 grid((T + kWarps - 1) / kWarps);
-  const size_t smem = (size_t)kWarps * std::max(E, 16) * sizeof(double);   // a warp: a row, or 32 slots; <= 32 KB
-  Groups gr{E / g.groups, 0};
-  if (gr.n % per == 0 && ((gr.n / per) & (gr.n / per - 1)) == 0) gr.span = gr.n / per;
-  auto go = [&](auto kernel, auto* l) {
-    kernel<<<grid, kWarps * 32, smem, c.stream>>>(l, bias, T, E, per, k, c.shared, c.s.renorm, g, gr, idx, w, c.ws.hdr);
+  const int T = (int)c.s.T, E = (int)c.routed_E, k = (int)c.routed_k;
+  auto go = [&](auto kernel, auto* l, int S) {
+    const int per = (E + S - 1) / S, tokens = kWarps * 32 / S;   // tokens of a block
+    // a warp's scratch in doubles: a row, the tokens' rows in floats, 32 slots
+    Groups gr{E / g.groups, 0, std::max(std::max(E, (32 / S * E + 1) / 2), 16)};
+    if (gr.n % per == 0 && ((gr.n / per) & (gr.n / per - 1)) == 0) gr.span = gr.n / per;
+    kernel<<<(T + tokens - 1) / tokens, kWarps * 32, (size_t)kWarps * gr.scratch * sizeof(double), c.stream>>>(
+        l, bias, T, E, per, k, c.shared, c.s.renorm, g, gr, idx, w, c.ws.hdr);
     return cudaGetLastError();
   };
   auto by_size = [&](auto* l, auto sig) {
     using L = std::remove_const_t<std::remove_pointer_t<decltype(l)>>;
     constexpr bool kSig = decltype(sig)::value;
-    if (per <= 4) return go(gate_kernel<L, kSig, 4>, l);
-    if (per <= 8) return go(gate_kernel<L, kSig, 8>, l);
-    if (per <= 16) return go(gate_kernel<L, kSig, 16>, l);
-    return go(gate_kernel<L, kSig, 32>, l);
+    // a lane for every slot and, where the keys are not exact, the best one left
+    const int lanes = std::max(k + (sizeof(L) == 2 && !bias ? 0 : 1), (int)g.groups);
+    if (T >= kManyTokens && lanes <= 8 && E <= 128)
+      return E <= 64 ? go(gate_kernel<L, kSig, 8, 8>, l, 8) : go(gate_kernel<L, kSig, 16, 8>, l, 8);
+    if (T >= kManyTokens && lanes <= 16 && E <= 256)
+      return E <= 128 ? go(gate_kernel<L, kSig, 8, 16>, l, 16) : go(gate_kernel<L, kSig, 16, 16>, l, 16);
+    if (E <= 128) return go(gate_kernel<L, kSig, 4, 32>, l, 32);
+    if (E <= 256) return go(gate_kernel<L, kSig, 8, 32>, l, 32);
+    if (E <= 512) return go(gate_kernel<L, kSig, 16, 32>, l, 32);
+    return go(gate_kernel<L, kSig, 32, 32>, l, 32);
   };
   auto by_score = [&](auto* l) {
     return g.score == MOE_SCORE_SIGMOID ? by_size(l, std::true_type()) : by_size(l, std::false_type());
@@ -595,19 +665,20 @@ cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits
 cudaError_t launch_gate_backward(const moe_shape& s, const moe_gate_desc& g, const void* logits, const int32_t* idx,
                                  const float* grad_w, void* grad_logits, cudaStream_t stream) {
   const int T = (int)s.T, E = (int)s.E, k = (int)s.topk, shared = (s.flags & MOE_FLAG_SHARED_EXPERT) ? 1 : 0;
-  const dim3 grid((T + kWarps - 1) / kWarps);
-  auto go = [&](auto kernel, auto* l, auto* d) {
-    kernel<<<grid, kWarps * 32, 0, stream>>>(l, idx, grad_w, T, E, k, shared, g.scale, d);
+  auto go = [&](auto kernel, auto* l, auto* d, int S) {
+    const int tokens = kWarps * 32 / S;
+    kernel<<<(T + tokens - 1) / tokens, kWarps * 32, 0, stream>>>(l, idx, grad_w, T, E, k, shared, g.scale, d);
     return cudaGetLastError();
   };
   auto by_size = [&](auto* l, auto* d, auto sig, auto ren) {
     using L = std::remove_pointer_t<decltype(d)>;
     constexpr bool kSig = decltype(sig)::value, kRen = decltype(ren)::value;
-    if (E % 4) return go(gate_backward_kernel<L, kSig, kRen, 32, 1>, l, d);
-    if (E <= 128) return go(gate_backward_kernel<L, kSig, kRen, 4, 4>, l, d);
-    if (E <= 256) return go(gate_backward_kernel<L, kSig, kRen, 8, 4>, l, d);
-    if (E <= 512) return go(gate_backward_kernel<L, kSig, kRen, 16, 4>, l, d);
-    return go(gate_backward_kernel<L, kSig, kRen, 32, 4>, l, d);
+    constexpr int kV = 16 / sizeof(L);
+    if (k <= 8 && T >= kManyTokens)
+      return E % kV == 0 ? go(gate_backward_kernel<L, kSig, kRen, 8, kV>, l, d, 8)
+                         : go(gate_backward_kernel<L, kSig, kRen, 8, 1>, l, d, 8);
+    return E % kV == 0 ? go(gate_backward_kernel<L, kSig, kRen, 32, kV>, l, d, 32)
+                       : go(gate_backward_kernel<L, kSig, kRen, 32, 1>, l, d, 32);
   };
   auto by_form = [&](auto* l, auto* d) {
     std::true_type yes;

@@ -125,55 +125,58 @@ FORMS = [
 
 
 @pytest.mark.parametrize("form", FORMS, ids=lambda f: "-".join(f"{k}{v}" for k, v in f.items()))
-@pytest.mark.parametrize("T", [1, 3, 257])
+@pytest.mark.parametrize("T", [1, 3, 257, 5003])
 def test_gate_matches_the_formulas(form, T):
     c = Case(T, **form)
     check(c, c.logits(T), c.make_bias())
 
 
+@pytest.mark.parametrize("T", [64, 4097])
 @pytest.mark.parametrize("dtype", [W.F32, W.BF16])
-def test_choice_at_a_border_binary32_cannot_see(dtype):
+def test_choice_at_a_border_binary32_cannot_see(dtype, T):
     """Choice scores that all lie within 2^-24 of one value: their order is
     only there in binary64."""
-    c = Case(64, E=128, k=8, score="sigmoid", bias=True, dtype=dtype)
+    c = Case(T, E=128, k=8, score="sigmoid", bias=True, dtype=dtype)
     logits = c.logits(5)
     logits[:] = logits[0]
-    flips = torch.arange(64, device="cuda") % 2 == 1
+    flips = torch.arange(T, device="cuda") % 2 == 1
     logits[flips] = logits[flips] * (1 + 2.0 ** -7)     # another value of either type
     bias = (0.75 - torch.sigmoid(logits[0].double())).float()
     check(c, logits, bias)
     # and groups whose two best sum to nearly the same
-    c = Case(64, E=128, k=8, score="sigmoid", bias=True, dtype=dtype, groups=8, topk_groups=4, best=2)
+    c = Case(T, E=128, k=8, score="sigmoid", bias=True, dtype=dtype, groups=8, topk_groups=4, best=2)
     check(c, logits, bias)
     # softmax scores of the same kind
-    c = Case(64, E=128, k=8, bias=True, dtype=dtype, groups=8, topk_groups=4)
+    c = Case(T, E=128, k=8, bias=True, dtype=dtype, groups=8, topk_groups=4)
     check(c, logits, (0.5 - torch.softmax(logits[0].double(), 0)).float())
 
 
+@pytest.mark.parametrize("T,k", [(48, 8), (4099, 8), (4099, 6)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("near", [2, 9, 20, 31, 32, 33, 100])
-def test_few_candidates_at_a_border(score, near):
+@pytest.mark.parametrize("near", [2, 9, 20, 31, 32, 33, 60])
+def test_few_candidates_at_a_border(score, near, T, k):
     """`near` experts within 2^-24 of one another around the last slot, the
     others clearly above (three) or below."""
-    c = Case(48, E=256, k=8, score=score, bias=True, renorm=0)
+    E = 256 if k == 8 else 96
+    c = Case(T, E=E, k=k, score=score, bias=True, renorm=0)
     logits = c.logits(near)
     logits[:] = logits[0]
     s = torch.sigmoid(logits[0].double()) if score == "sigmoid" else torch.softmax(logits[0].double(), 0)
     gen = torch.Generator().manual_seed(near)
-    order = torch.randperm(256, generator=gen)
-    target = torch.full((256,), 0.25, dtype=torch.float64)
+    order = torch.randperm(E, generator=gen)
+    target = torch.full((E,), 0.25, dtype=torch.float64)
     target[order[:3]] = torch.tensor([1.5, 1.25, 1.125], dtype=torch.float64)
     target[order[3:3 + near]] = 0.75
     bias = (target.cuda() - s).float()
     # the same bits in another order of rows: each row moves one logit by a unit
-    for t in range(48):
-        logits[t, order[3 + t % near]] *= 1 + 2.0 ** -23
+    t = torch.arange(T)
+    logits[t, order[3 + t % near]] *= 1 + 2.0 ** -23
     check(c, logits, bias)
     # and on the logits themselves: neighbouring binary32 numbers
-    c = Case(48, E=256, k=8, score=score)
-    l = torch.full((48, 256), -1.0)
+    c = Case(T, E=E, k=k, score=score)
+    l = torch.full((T, E), -1.0)
     l[:, order[:3]] = 2.0
-    steps = torch.randint(0, 8, (48, near), generator=gen).float()
+    steps = torch.randint(0, 8, (T, near), generator=gen).float()
     l[:, order[3:3 + near]] = 1 + steps * 2.0 ** -23
     check(c, l.cuda())
 
@@ -227,10 +230,11 @@ def test_shape_without_tokens():
     c.back(z, torch.empty(0, 4, dtype=torch.int32, device="cuda"), torch.empty(0, 4, device="cuda"))
 
 
+@pytest.mark.parametrize("T", [3, 4097])
 @pytest.mark.parametrize("where", ["logit", "bias"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
-def test_nonfinite_values_are_latched(where, value):
-    c = Case(3, E=64, k=4, score="sigmoid", bias=True)
+def test_nonfinite_values_are_latched(where, value, T):
+    c = Case(T, E=64, k=4, score="sigmoid", bias=True, groups=4, topk_groups=2, best=2)
     logits, bias = c.logits(), c.make_bias()
     if where == "logit":
         logits[1, 63] = value
@@ -238,12 +242,10 @@ def test_nonfinite_values_are_latched(where, value):
         bias[17] = value
     idx, w = c.run(logits, bias)
     assert moe.moe_poll_status(c.ws) == 6
-    bad = [1] if where == "logit" else [0, 1, 2]
-    for t in range(3):
-        if t in bad:
-            assert idx[t].tolist() == [0, 1, 2, 3] and bool(torch.isnan(w[t]).all())
-        else:
-            assert bool(torch.isfinite(w[t]).all())
+    bad = torch.zeros(T, dtype=torch.bool) if where == "logit" else torch.ones(T, dtype=torch.bool)
+    bad[1] = True
+    assert bool((idx.cpu()[bad] == torch.arange(4)).all()) and bool(torch.isnan(w.cpu()[bad]).all())
+    assert bool(torch.isfinite(w.cpu()[~bad]).all())
     assert moe.moe_poll_status(c.ws) == 0      # read once
 
 
@@ -266,7 +268,7 @@ def _grad_formula(c, logits, idx, gw):
 
 @pytest.mark.parametrize("form", [f for f in FORMS if not f.get("shared")],
                          ids=lambda f: "-".join(f"{k}{v}" for k, v in f.items()))
-@pytest.mark.parametrize("T", [1, 130])
+@pytest.mark.parametrize("T", [1, 130, 4999])
 def test_gradient_matches_the_formula(form, T):
     c = Case(T, **form)
     logits, bias = c.logits(7), c.make_bias()
@@ -297,14 +299,16 @@ def test_gradient_matches_differences(score, renorm):
         assert torch.allclose(got[:, e], diff, rtol=0, atol=6 * 1.5 * h * h * 4 + 2 * tol(l) * 12)
 
 
+@pytest.mark.parametrize("rep", [1, 1000])
 @pytest.mark.parametrize("score,renorm", [("softmax", 0), ("softmax", 1), ("sigmoid", 0), ("sigmoid", 1)])
-def test_gradient_of_absent_and_repeated_slots(score, renorm):
-    c = Case(5, E=16, k=4, score=score, renorm=renorm)
-    logits = c.logits(11)
+def test_gradient_of_absent_and_repeated_slots(score, renorm, rep):
+    c = Case(5 * rep, E=16, k=4, score=score, renorm=renorm)
+    logits = c.logits(11)[:5].repeat(rep, 1)
     idx = torch.tensor([[3, -1, 16, 5], [2, 2, 7, 2], [-1, -1, -1, -1], [1 << 30, 0, -(1 << 31), 15], [9, 9, 9, 9]],
                        dtype=torch.int32, device="cuda")
     gw = torch.randn(5, 4, generator=torch.Generator().manual_seed(4)).cuda()
-    got = c.back(logits, idx, gw).double().cpu()
+    got = c.back(logits, idx.repeat(rep, 1), gw.repeat(rep, 1)).double().cpu()
+    assert torch.equal(got, got[:5].repeat(rep, 1))
     for t in range(5):
         keep = [j for j in range(4) if 0 <= int(idx[t, j]) < 16]
         if not keep:
