@@ -125,13 +125,13 @@ FORMS = [
 
 
 @pytest.mark.parametrize("form", FORMS, ids=lambda f: "-".join(f"{k}{v}" for k, v in f.items()))
-@pytest.mark.parametrize("T", [1, 3, 257, 5003])
+@pytest.mark.parametrize("T", [1, 3, 257, 8195])
 def test_gate_matches_the_formulas(form, T):
     c = Case(T, **form)
     check(c, c.logits(T), c.make_bias())
 
 
-@pytest.mark.parametrize("T", [64, 4097])
+@pytest.mark.parametrize("T", [64, 32769])
 @pytest.mark.parametrize("dtype", [W.F32, W.BF16])
 def test_choice_at_a_border_binary32_cannot_see(dtype, T):
     """Choice scores that all lie within 2^-24 of one value: their order is
@@ -151,7 +151,7 @@ def test_choice_at_a_border_binary32_cannot_see(dtype, T):
     check(c, logits, (0.5 - torch.softmax(logits[0].double(), 0)).float())
 
 
-@pytest.mark.parametrize("T,k", [(48, 8), (4099, 8), (4099, 6)])
+@pytest.mark.parametrize("T,k", [(48, 8), (32771, 8), (8195, 6)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("near", [2, 9, 20, 31, 32, 33, 60])
 def test_few_candidates_at_a_border(score, near, T, k):
@@ -230,7 +230,7 @@ def test_shape_without_tokens():
     c.back(z, torch.empty(0, 4, dtype=torch.int32, device="cuda"), torch.empty(0, 4, device="cuda"))
 
 
-@pytest.mark.parametrize("T", [3, 4097])
+@pytest.mark.parametrize("T", [3, 8193])
 @pytest.mark.parametrize("where", ["logit", "bias"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
 def test_nonfinite_values_are_latched(where, value, T):
