@@ -2,56 +2,212 @@
 // rounded to nearest even. The reciprocal, the product and the quotient are
 // correctly rounded ones, so that the result is defined to the bit.
 //
-// One block per row (of all rows, or of the filled rows of windows).
+// Bound by HBM: 3 bytes an element of bf16 rows (5 of fp32), read once. A team
+// of threads (part of a warp, a warp, or a block of four for rows beyond 8 KB)
+// keeps its row in registers between the maximum and the quantisation, 16 bytes
+// a thread and step; what a row has beyond the registers is read again. Warps
+// with rows of their own meet no barrier, and while some reduce, the others'
+// loads are in flight.
+//
+// A correctly rounded quotient costs some twenty instructions, which would be
+// the bound instead. It is only needed next to a tie: f = rint(x * inv), inv the
+// rounded reciprocal of scale, is x / scale rounded wherever x * inv is not
+// within 1.2e-5 of a half (inv is off by 2^-24 relative, the defined quotient by
+// another 2^-25, of at most 127). A thread with an element closer than 2e-5
+// divides its step. rint is a sum with 1.5 * 2^23, whose low byte is q.
 #include "moe_internal.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kMaxExperts = 1024;
 
+// 16 bytes of consecutive elements, as loaded.
 template <typename T>
-__device__ __forceinline__ float load_x(const T* p) {
-  if constexpr (sizeof(T) == 2) return __bfloat162float(*p);
-  else return *p;
-}
+struct Piece {
+  static constexpr int kN = 16 / sizeof(T);
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const T* p) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+  // |x| as bits: ordered like the values, NaN and infinity above all numbers
+  __device__ __forceinline__ uint32_t most(uint32_t m) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFF0000u, (w[i] << 16) & 0x7FFF0000u));
+    }
+    return m;
+  }
+  __device__ __forceinline__ void quantise(float s, float inv, int8_t* q) const {
+    constexpr float kMagic = 12582912.f;   // 1.5 * 2^23
+    float t[kN], far = 0.f;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const float x = at(i);
+      t[i] = __fmaf_rn(x, inv, kMagic);
+      far = fmaxf(far, fabsf(__fmaf_rn(x, inv, kMagic - t[i])));
+    }
+    if (far > 0.49998f) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) t[i] = kMagic + rintf(__fdiv_rn(at(i), s));
+    }
+    uint32_t b[kN / 4];
+#pragma unroll
+    for (int i = 0; i < kN / 4; ++i)
+      b[i] = __byte_perm(__byte_perm(__float_as_uint(t[4 * i]), __float_as_uint(t[4 * i + 1]), 0x0040),
+                         __byte_perm(__float_as_uint(t[4 * i + 2]), __float_as_uint(t[4 * i + 3]), 0x0040), 0x5410);
+    store(b, q);
+  }
+  static __device__ __forceinline__ void store(const uint32_t (&b)[kN / 4], int8_t* q) {   // kN codes
+    if constexpr (kN == 8) *reinterpret_cast<uint2*>(q) = make_uint2(b[0], b[1]);
+    else *reinterpret_cast<uint32_t*>(q) = b[0];
+  }
+};
 
-template <typename T>
+// kTeam threads a row, kKeep steps of it in registers.
+template <typename T, int kTeam, int kKeep>
 __global__ void __launch_bounds__(kThreads)
 quant_i8_kernel(const T* __restrict__ x, int64_t rows, int cols, RowWindows win, int8_t* __restrict__ q,
                 float* __restrict__ scale) {
-  __shared__ uint32_t part[kThreads / 32];
-  int64_t row0;
-  const int n = window_rows(win, blockIdx.y, rows, &row0);
-  for (int r = blockIdx.x; r < n; r += gridDim.x) {
-    const T* xr = x + (row0 + r) * cols;
-    // |x| as bits: ordered like the values, NaN and infinity above all numbers
-    uint32_t m = 0;
-    for (int i = threadIdx.x; i < cols; i += kThreads) m = max(m, __float_as_uint(load_x(xr + i)) & 0x7FFFFFFFu);
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __shared__ uint32_t part[2][kThreads / 32];
+  __shared__ int first[kMaxExperts + 1];   // rows of the windows before each window
+  const int tid = threadIdx.x % kTeam, lane = threadIdx.x & 31;
+  int total = (int)rows;
+  if (win.offsets) {
+    if (threadIdx.x < 32) {
+      int at = 0;
+      for (int e0 = 0; e0 < win.experts; e0 += 32) {
+        int64_t row0;
+        const int n = e0 + lane < win.experts ? window_rows(win, e0 + lane, rows, &row0) : 0;
+        int inc = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, inc, off);
+          if (lane >= off) inc += v;
+        }
+        if (e0 + lane < win.experts) first[e0 + lane] = at + inc - n;
+        at += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      if (lane == 0) first[win.experts] = at;
+    }
     __syncthreads();
-    for (int i = 0; i < kThreads / 32; ++i) m = max(m, part[i]);
-    __syncthreads();
-    const bool bad = m >= 0x7F800000u;
-    const float s = bad ? __int_as_float(0x7fc00000) : (m == 0 ? 1.f : fmaxf(__fmul_rn(__uint_as_float(m), 1.f / 127.f), 0x1p-126f));
-    if (threadIdx.x == 0) scale[row0 + r] = s;
-    for (int i = threadIdx.x; i < cols; i += kThreads)
-      q[(row0 + r) * cols + i] = bad ? 0 : (int8_t)__float2int_rn(__fdiv_rn(load_x(xr + i), s));
+    total = first[win.experts];
   }
+  constexpr int kTeams = kThreads / kTeam;
+  int turn = 0;
+  for (int64_t i0 = (int64_t)blockIdx.x * kTeams + threadIdx.x / 32 * (kTeam < 32 ? 32 / kTeam : 1) / (kTeam > 32 ? kTeam / 32 : 1);
+       i0 < total; i0 += (int64_t)gridDim.x * kTeams, turn ^= 1) {
+    // teams of one warp past the last row do that row once more, without storing
+    const int64_t mine = i0 + (kTeam < 32 ? lane / kTeam : 0), i = mine < total ? mine : total - 1;
+    const bool real = mine < total;
+    int64_t r = i;
+    if (win.offsets) {   // the last window that starts at or before row i (empty ones never do)
+      int lo = 0, hi = win.experts - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= i) lo = mid;
+        else hi = mid - 1;
+      }
+      r = (int64_t)__ldg(win.offsets + lo) + (i - first[lo]);
+    }
+    const T* xr = x + r * cols;
+    int8_t* qr = q + r * cols;
+    Piece<T> kept[kKeep];
+    uint32_t m = 0;
+#pragma unroll
+    for (int g = 0; g < kKeep; ++g) {
+      const int c = (g * kTeam + tid) * Piece<T>::kN;
+      if (c < cols) kept[g].load(xr + c);
+      else kept[g].zero();
+    }
+#pragma unroll
+    for (int g = 0; g < kKeep; ++g) m = kept[g].most(m);
+    for (int c = (kKeep * kTeam + tid) * Piece<T>::kN; c < cols; c += kTeam * Piece<T>::kN) {
+      Piece<T> more;
+      more.load(xr + c);
+      m = more.most(m);
+    }
+    if constexpr (kTeam >= 32) {
+      m = __reduce_max_sync(0xffffffffu, m);
+    } else {
+#pragma unroll
+      for (int off = kTeam / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+    }
+    if constexpr (kTeam > 32) {   // two slots in turn: one barrier a row
+      if (lane == 0) part[turn][threadIdx.x >> 5] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kTeam / 32; ++w) m = max(m, part[turn][w]);
+    }
+    const bool bad = m >= 0x7F800000u;
+    const float s = bad ? __int_as_float(0x7fc00000)
+                        : (m == 0 ? 1.f : fmaxf(__fmul_rn(__uint_as_float(m), 1.f / 127.f), 0x1p-126f));
+    const float inv = __frcp_rn(s);
+    if (!real) continue;
+    if (tid == 0) scale[r] = s;
+    auto put = [&](const Piece<T>& v, int c) {
+      if (bad) {
+        const uint32_t none[Piece<T>::kN / 4] = {};
+        Piece<T>::store(none, qr + c);
+      } else {
+        v.quantise(s, inv, qr + c);
+      }
+    };
+#pragma unroll
+    for (int g = 0; g < kKeep; ++g) {
+      const int c = (g * kTeam + tid) * Piece<T>::kN;
+      if (c < cols) put(kept[g], c);
+    }
+    for (int c = (kKeep * kTeam + tid) * Piece<T>::kN; c < cols; c += kTeam * Piece<T>::kN) {
+      Piece<T> more;
+      more.load(xr + c);
+      put(more, c);
+    }
+  }
+}
+
+template <typename T, int kTeam, int kKeep>
+cudaError_t go(int64_t rows, int64_t cols, const void* x, const RowWindows& win, int8_t* q, float* scale, int num_sms,
+               cudaStream_t stream) {
+  const int64_t need = ceil_div(rows, kThreads / kTeam), most = 16 * (int64_t)num_sms;
+  quant_i8_kernel<T, kTeam, kKeep>
+      <<<(unsigned)(need < most ? need : most), kThreads, 0, stream>>>((const T*)x, rows, (int)cols, win, q, scale);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t by_cols(int64_t rows, int64_t cols, const void* x, const RowWindows& win, int8_t* q, float* scale,
+                    int num_sms, cudaStream_t stream) {
+  const int64_t bytes = cols * (int64_t)sizeof(T);
+  // few rows: a block each, so that one row is not one warp's work
+  const bool few = rows < 4 * (int64_t)num_sms;
+  if (bytes <= 256 && !few) return go<T, 8, 2>(rows, cols, x, win, q, scale, num_sms, stream);
+  if (bytes <= 1024) return go<T, 32, 2>(rows, cols, x, win, q, scale, num_sms, stream);
+  if (!few) {
+    if (bytes <= 2048) return go<T, 32, 4>(rows, cols, x, win, q, scale, num_sms, stream);
+    if (bytes <= 4096) return go<T, 32, 8>(rows, cols, x, win, q, scale, num_sms, stream);
+    if (bytes <= 8192) return go<T, 32, 16>(rows, cols, x, win, q, scale, num_sms, stream);
+  }
+  if (bytes <= 16384) return go<T, 128, 8>(rows, cols, x, win, q, scale, num_sms, stream);
+  return go<T, 128, 16>(rows, cols, x, win, q, scale, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_quant_i8(int64_t rows, int64_t cols, int32_t dtype, const void* x, const RowWindows& win,
                             int8_t* q, float* scale, int num_sms, cudaStream_t stream) {
-  const int64_t most = (8 * num_sms + win.experts - 1) / win.experts;
-  const dim3 grid((unsigned)(rows < most ? rows : most), win.experts);
-  if (dtype == MOE_BF16)
-    quant_i8_kernel<<<grid, kThreads, 0, stream>>>((const __nv_bfloat16*)x, rows, (int)cols, win, q, scale);
-  else
-    quant_i8_kernel<<<grid, kThreads, 0, stream>>>((const float*)x, rows, (int)cols, win, q, scale);
-  return cudaGetLastError();
+  return dtype == MOE_BF16 ? by_cols<__nv_bfloat16>(rows, cols, x, win, q, scale, num_sms, stream)
+                           : by_cols<float>(rows, cols, x, win, q, scale, num_sms, stream);
 }
 
 }  // namespace moe
