@@ -9,12 +9,14 @@
 // with rows of their own meet no barrier, and while some reduce, the others'
 // loads are in flight.
 //
-// A correctly rounded quotient costs some twenty instructions, which would be
-// the bound instead. It is only needed next to a tie: f = rint(x * inv), inv the
-// rounded reciprocal of scale, is x / scale rounded wherever x * inv is not
-// within 1.2e-5 of a half (inv is off by 2^-24 relative, the defined quotient by
-// another 2^-25, of at most 127). A thread with an element closer than 2e-5
-// divides its step. rint is a sum with 1.5 * 2^23, whose low byte is q.
+// A division instruction sequence costs some twenty instructions an element,
+// which would be the bound instead. With y the rounded reciprocal of s, one a
+// row, q0 = x y is within two units of the quotient, q1 = q0 + (x - q0 s) y
+// within one, and q2 = q1 + (x - q1 s) y, each an fma, is then the correctly
+// rounded quotient (Markstein's theorem: y correctly rounded, q1 within one
+// unit, the remainder exact). Rows whose remainders could leave the normal
+// numbers are scaled by 2^64 first, which changes no quotient. Adding
+// 1.5 * 2^23 rounds to an integer, ties to even, whose low byte is the code.
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -48,18 +50,16 @@ struct Piece {
     }
     return m;
   }
-  __device__ __forceinline__ void quantise(float s, float inv, int8_t* q) const {
-    constexpr float kMagic = 12582912.f;   // 1.5 * 2^23
-    float t[kN], far = 0.f;
+  template <bool kTiny>
+  __device__ __forceinline__ void quantise(float s, float y, int8_t* q) const {
+    float t[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const float x = at(i);
-      t[i] = __fmaf_rn(x, inv, kMagic);
-      far = fmaxf(far, fabsf(__fmaf_rn(x, inv, kMagic - t[i])));
-    }
-    if (far > 0.49998f) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) t[i] = kMagic + rintf(__fdiv_rn(at(i), s));
+      const float x = kTiny ? at(i) * 0x1p64f : at(i);
+      float v = __fmul_rn(x, y);
+      v = __fmaf_rn(__fmaf_rn(-v, s, x), y, v);
+      v = __fmaf_rn(__fmaf_rn(-v, s, x), y, v);
+      t[i] = __fadd_rn(v, 12582912.f);   // 1.5 * 2^23
     }
     uint32_t b[kN / 4];
 #pragma unroll
@@ -76,7 +76,7 @@ struct Piece {
 
 // kTeam threads a row, kKeep steps of it in registers.
 template <typename T, int kTeam, int kKeep>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kKeep <= 8 ? 8 : 5)
 quant_i8_kernel(const T* __restrict__ x, int64_t rows, int cols, RowWindows win, int8_t* __restrict__ q,
                 float* __restrict__ scale) {
   __shared__ uint32_t part[2][kThreads / 32];
@@ -152,15 +152,18 @@ quant_i8_kernel(const T* __restrict__ x, int64_t rows, int cols, RowWindows win,
     const bool bad = m >= 0x7F800000u;
     const float s = bad ? __int_as_float(0x7fc00000)
                         : (m == 0 ? 1.f : fmaxf(__fmul_rn(__uint_as_float(m), 1.f / 127.f), 0x1p-126f));
-    const float inv = __frcp_rn(s);
+    const bool tiny = s < 0x1p-60f;
+    const float up = tiny ? s * 0x1p64f : s, y = __frcp_rn(up);
     if (!real) continue;
     if (tid == 0) scale[r] = s;
     auto put = [&](const Piece<T>& v, int c) {
       if (bad) {
         const uint32_t none[Piece<T>::kN / 4] = {};
         Piece<T>::store(none, qr + c);
+      } else if (tiny) {
+        v.template quantise<true>(up, y, qr + c);
       } else {
-        v.quantise(s, inv, qr + c);
+        v.template quantise<false>(up, y, qr + c);
       }
     };
 #pragma unroll

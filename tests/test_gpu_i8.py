@@ -91,6 +91,39 @@ def test_quant_ties_zeros_and_far_values():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quant_rounds_next_to_ties(dtype):
+    """Elements at, and a unit beside, x = (n + 1/2) scale, of rows with scales
+    over the whole exponent range."""
+    g = gen(7)
+    rows, cols = 3000, 1024
+    amax = (torch.rand(rows, 1, generator=g) + 1) * torch.exp2(torch.randint(-149, 127, (rows, 1), generator=g).double())
+    amax = amax.float().to(DT[dtype]).float()
+    scale = torch.maximum(amax * (torch.tensor(1.0) / torch.tensor(127.0)), torch.tensor(2.0 ** -126))
+    n = torch.randint(-127, 127, (rows, cols), generator=g)
+    x = ((n + 0.5).double() * scale.double()).float()
+    step = torch.randint(-2, 3, (rows, cols), generator=g, dtype=torch.int32)
+    x = (x.view(torch.int32) + step).view(torch.float32)     # neighbouring numbers
+    x = x.to(DT[dtype]).float()
+    x = torch.where(torch.isfinite(x) & (x.abs() <= amax), x, torch.zeros(()))
+    x[:, 77] = amax[:, 0]
+    x = x.to(DT[dtype]).cuda()
+    q, s = run_quant(x)
+    rq, rs = quant_ref(x)
+    assert np.array_equal(s, rs) and np.array_equal(q, rq)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(9, 16), (9, 528), (2000, 64), (2000, 2048), (700, 8192), (5, 40000)])
+def test_quant_of_rows_that_are_not_finite(dtype, rows, cols):
+    x = torch.randn(rows, cols, generator=gen(3))
+    x[::4, -1], x[1::4, 0], x[2::4, cols // 2] = float("nan"), float("inf"), float("-inf")
+    x = x.to(DT[dtype]).cuda()
+    q, s = run_quant(x)
+    rq, rs = quant_ref(x)
+    assert np.array_equal(s, rs, equal_nan=True) and np.array_equal(q, rq)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_quant_of_windows_leaves_other_rows(dtype):
     M, K = 900, 272
     x = torch.randn(M, K, generator=gen(5)).to(DT[dtype]).cuda()
