@@ -74,6 +74,15 @@ struct Params {
   int tiles;     // channel tiles of one expert
 };
 
+// g / (1 + exp(-g)) for results rounded to bf16: off by a few 2^-22 relative,
+// and by 1.6 |g| 2^-24 from the exponent (exactly g or 0 far out).
+__device__ __forceinline__ float quick_silu(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return g * r;
+}
+
 // One unit: chunk `chunk` of expert e's rows, channel tile `tile`.
 struct Unit {
   int e, tile, rows;
@@ -144,30 +153,30 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
   else __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int64_t units = (int64_t)tab[E] * p.tiles;
+  const int units = tab[E] * p.tiles;   // below 2^31 (checked by the ABI)
 
   auto remote = [&](const void* q, uint32_t r) { return ptx::mapa_shared(ptx::smem_u32(q), r); };
 
   // Unit u. Within an expert: bands of kBand chunks, in a band channel tile by
   // channel tile, so that the workers of one moment share few rows and few
   // channels in L2.
-  auto unit = [&](int64_t u) -> Unit {
-    const int64_t nt = p.tiles;
+  auto unit = [&](int u) -> Unit {
+    const uint32_t nt = (uint32_t)p.tiles;
     int lo = 0, hi = E - 1;   // the last expert whose first unit is <= u (empty ones never are)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (tab[mid] * nt <= u) lo = mid;
+      if ((uint32_t)tab[mid] * nt <= (uint32_t)u) lo = mid;
       else hi = mid - 1;
     }
     const int nc = tab[lo + 1] - tab[lo];
-    const int64_t v = u - tab[lo] * nt;
-    const int64_t band = v / (kBand * nt), w = v - band * kBand * nt;
+    const uint32_t v = (uint32_t)u - (uint32_t)tab[lo] * nt;
+    const uint32_t band = v / (kBand * nt), w = v - band * kBand * nt;
     const int left = nc - (int)band * kBand;
-    const int bh = left < kBand ? left : kBand;
-    const int chunk = (int)band * kBand + (int)(w % bh);
+    const uint32_t bh = (uint32_t)(left < kBand ? left : kBand);
     Unit r;
     r.e = lo;
     r.tile = (int)(w / bh);
+    const int chunk = (int)(band * kBand + w - (uint32_t)r.tile * bh);
     int64_t row0;
     const int rows = window_rows(p.win, lo, p.M, &row0) - chunk * F::kRows;
     r.rows = rows < F::kRows ? rows : F::kRows;
@@ -188,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     uint32_t armed = 0, armed_parity = 0;
     const uint64_t pol = kG == 2 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
     bool ok = true;
-    for (int64_t u = worker; ok && u < units; u += workers) {
+    for (int u = worker; ok && u < units; u += workers) {
       const Unit j = unit(u);
       const int n = columns(j.rows) / kG;                       // rows this CTA loads
       const int wrow = (int)(j.e * p.N + (int64_t)j.tile * (kG * F::kCh) + rank * F::kCh);
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     if (rank == 0) {
       uint32_t stage = 0, phase = 0, i = 0;
       bool ok = true;
-      for (int64_t u = worker; ok && u < units; u += workers, ++i) {
+      for (int u = worker; ok && u < units; u += workers, ++i) {
         const uint32_t slot = i & 1u, use = (i >> 1) & 1u;
         int good = 1;
         if (lane == 0) good = wait_bar<kG == 2>(acc_empty + slot, use ^ 1u, abort_flag, p.hdr, 0x58000000u | slot);
@@ -305,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     int* xu = xg + 16 * 64;
     float* xs_all = reinterpret_cast<float*>(smem + F::kOffXs);
     uint32_t i = 0;
-    for (int64_t u = worker; u < units; u += workers, ++i) {
+    for (int u = worker; u < units; u += workers, ++i) {
       const Unit j = unit(u);
       const uint32_t slot = i & 1u, use = (i >> 1) & 1u;
       float* xs = xs_all + slot * F::kRows;
@@ -321,21 +330,53 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
       while (!ptx::mbar_try_wait(acc_full + slot, use)) {}   // completed: returns at once
       ptx::tc_fence_after();
       const uint32_t d = tmem + slot * F::kRows + ((uint32_t)(q * 32) << 16);
+      const int64_t tile0 = n0 - ch;   // the CTA's first channel
+      // bf16: two lanes exchange half of their rows, so that each stores two
+      // neighbouring channels at once
+      const bool pairs = sizeof(O) == 2 && (p.N & 1) == 0 && tile0 + F::kCh <= p.N;
       O* y = reinterpret_cast<O*>(p.y) + j.row * p.N + n0;
-      auto store = [&](int c, float v) {
-        if (c < j.rows && real) {
-          if constexpr (sizeof(O) == 2) y[(int64_t)c * p.N] = __float2bfloat16_rn(v);
-          else y[(int64_t)c * p.N] = v;
+      // rows c .. c + 15 of this thread's channel
+      auto store16 = [&](int c, const float (&f)[16]) {
+        if (pairs && c + 16 <= j.rows) {
+          const bool odd = lane & 1;
+          O* q = y + (int64_t)(c + (odd ? 1 : 0)) * p.N - (odd ? 1 : 0);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? f[i] : f[i + 1], 1);
+            const __nv_bfloat162 two = __floats2bfloat162_rn(odd ? got : f[i], odd ? f[i + 1] : got);
+            *reinterpret_cast<__nv_bfloat162*>(q) = two;
+            q += 2 * p.N;
+          }
+        } else if (real) {
+          O* q = y + (int64_t)c * p.N;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c + i < j.rows) {
+              if constexpr (sizeof(O) == 2) *q = __float2bfloat16_rn(f[i]);
+              else *q = f[i];
+            }
+            q += p.N;
+          }
         }
       };
       for (int c0 = 32 * set; c0 < j.rows; c0 += 64) {
         uint32_t v[32];
         ptx::tmem_ld_x32(d + c0, v);
         ptx::tmem_wait_ld();
+        float f[16];
         if constexpr (!kUp) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (c0 + c < j.rows) store(c0 + c, (float)(int)v[c] * sw * xs[c0 + c]);
+          for (int h = 0; h < 32; h += 16) {
+            if (c0 + h >= j.rows) break;
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) {
+              const float4 s = *reinterpret_cast<const float4*>(xs + c0 + h + c);
+              f[c] = (float)(int)v[h + c] * sw * s.x;
+              f[c + 1] = (float)(int)v[h + c + 1] * sw * s.y;
+              f[c + 2] = (float)(int)v[h + c + 2] * sw * s.z;
+              f[c + 3] = (float)(int)v[h + c + 3] * sw * s.w;
+            }
+            store16(c0 + h, f);
           }
         } else {
           // gate warps finish the batch's first 16 columns, up warps the last
@@ -346,14 +387,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
             else xu[c * 64 + ch] = (int)v[c];
           }
           ptx::named_barrier(2 + set, 128);
+          const int first = c0 + (gate ? 0 : 16);
+          if (first < j.rows) {
+            const int* other = gate ? xu : xg;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int col = c0 + (gate ? c : 16 + c);
-            if (col < j.rows) {
-              const int gi = gate ? (int)v[c] : xg[c * 64 + ch], ui = gate ? xu[c * 64 + ch] : (int)v[16 + c];
-              const float s = xs[col], g = (float)gi * sw * s;
-              store(col, g / (1.f + expf(-g)) * ((float)ui * su * s));
+            for (int c = 0; c < 16; c += 4) {
+              const float4 s4 = *reinterpret_cast<const float4*>(xs + first + c);
+              const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int own = (int)(gate ? v[c + i] : v[16 + c + i]), far = other[(c + i) * 64 + ch];
+                const float g = (float)(gate ? own : far) * sw * s[i], u = (float)(gate ? far : own) * su * s[i];
+                f[c + i] = (sizeof(O) == 2 ? quick_silu(g) : g / (1.f + expf(-g))) * u;
+              }
             }
+            store16(first, f);
           }
           ptx::named_barrier(2 + set, 128);
         }

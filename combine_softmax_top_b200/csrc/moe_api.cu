@@ -460,6 +460,7 @@ moe_status moe_gemm_i8(const moe_gemm_i8_desc* d, const int8_t* x, const float* 
   if (!d || d->reserved != 0 || d->M < 0 || d->M > INT32_MAX || d->N < 1 || d->K < 16 || d->K > 131056 ||
       d->K % 16 != 0 || d->fill < 0 || d->experts < 1 || d->experts > 1024 || d->N > INT32_MAX / d->experts)
     return MOE_ERR_INVALID_ARG;
+  if ((ceil_div(d->M, 64) + d->experts) > INT32_MAX / ceil_div(d->N, 64)) return MOE_ERR_INVALID_ARG;
   if (!is_dtype(d->out_dtype)) return MOE_ERR_INVALID_ARG;
   if (d->out_dtype == MOE_E4M3) return MOE_ERR_UNSUPPORTED;
   const bool dense = d->experts == 1 && !offsets && !counts;

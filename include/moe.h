@@ -520,7 +520,8 @@ MOE_API moe_status moe_quant_i8(int64_t rows, int64_t cols, int32_t src_dtype, c
 
 typedef struct moe_gemm_i8_desc {
   int64_t M;         /* rows of x and y, 0 .. 2^31 - 1 */
-  int64_t N;         /* output channels of one expert, >= 1; experts * N < 2^31 */
+  int64_t N;         /* output channels of one expert, >= 1; experts * N < 2^31,
+                        and (M / 64 + experts) * N / 64, each rounded up, < 2^31 */
   int64_t K;         /* a multiple of 16, 16 .. 131056: the sums stay below 2^31 */
   int64_t experts;   /* 1..1024; windows need offsets and counts, 1 without them is a dense product */
   int64_t fill;      /* rows expected to be filled over all windows, 0 = M: chooses the

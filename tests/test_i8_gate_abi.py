@@ -90,6 +90,7 @@ def _gemm(M=4, N=128, K=128, experts=1, fill=0, out=moe.MOE_BF16, reserved=0, x=
 
 
 @pytest.mark.parametrize("over,code", [
+    (dict(M=(1 << 31) - 1, N=1 << 12), INVALID),
     (dict(M=-1), INVALID), (dict(M=1 << 31), INVALID), (dict(N=0), INVALID), (dict(N=1 << 31), INVALID),
     (dict(K=0), INVALID), (dict(K=24), INVALID), (dict(K=131072), INVALID), (dict(fill=-1), INVALID),
     (dict(reserved=1), INVALID), (dict(out=moe.MOE_E4M3), UNSUPPORTED), (dict(out=11), INVALID),
