@@ -5,7 +5,7 @@
 //
 // The weights are the MMA's A operand (M = 128 channels a CTA) and the rows its
 // N operand, so a few rows cost few columns. A unit of work is (expert, channel
-// tile, chunk of up to kRows rows); a persistent grid takes the units in a
+// tile, chunk of up to kRows rows, the expert's chunks being alike); a persistent grid takes the units in a
 // fixed order, which every warp derives by itself from the windows. With an up
 // projection a CTA's 128 A rows are 64 gate and 64 up channels, and the
 // epilogue brings the two halves of tensor memory together through shared
@@ -62,7 +62,7 @@ struct Form {
 
 struct Params {
   CUtensorMap tm_w, tm_wu;   // [experts * N, K], boxes of 128 (64 with up) channels
-  CUtensorMap tm_x, tm_x16;  // [M, K], boxes of kBRows and 16 rows
+  CUtensorMap tm_x[4];       // [M, K], boxes of 16, 32, 64 and 128 rows
   const float* xs;
   const float* ws;
   const float* wus;
@@ -157,6 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
 
   auto remote = [&](const void* q, uint32_t r) { return ptx::mapa_shared(ptx::smem_u32(q), r); };
 
+  // MMA columns for that many rows
+  auto columns = [](int rows) { return (rows + 16 * kG - 1) / (16 * kG) * (16 * kG); };
   // Unit u. Within an expert: bands of kBand chunks, in a band channel tile by
   // channel tile, so that the workers of one moment share few rows and few
   // channels in L2.
@@ -178,19 +180,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     r.tile = (int)(w / bh);
     const int chunk = (int)(band * kBand + w - (uint32_t)r.tile * bh);
     int64_t row0;
-    const int rows = window_rows(p.win, lo, p.M, &row0) - chunk * F::kRows;
-    r.rows = rows < F::kRows ? rows : F::kRows;
-    r.row = row0 + (int64_t)chunk * F::kRows;
+    // an expert's chunks are of one size, so that the units that follow one
+    // another cost alike (256 + 14 rows: 160 + 110)
+    const int rows = window_rows(p.win, lo, p.M, &row0);
+    const int each = columns((int)(((uint32_t)rows + (uint32_t)nc - 1u) / (uint32_t)nc));
+    const int left_rows = rows - chunk * each;
+    r.rows = left_rows < each ? left_rows : each;
+    r.row = row0 + (int64_t)chunk * each;
     return r;
   };
-  auto columns = [](int rows) { return (rows + 16 * kG - 1) / (16 * kG) * (16 * kG); };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer (both CTAs)
     if (lane == 0) {
       ptx::prefetch_tmap(&p.tm_w);
-      ptx::prefetch_tmap(&p.tm_x);
-      ptx::prefetch_tmap(&p.tm_x16);
+      for (int b = 0; b < 4; ++b) ptx::prefetch_tmap(&p.tm_x[b]);
       if (kUp) ptx::prefetch_tmap(&p.tm_wu);
     }
     uint32_t stage = 0, phase = 0;
@@ -211,25 +215,25 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
         if (ptx::elect_one()) {
           if (rank == 0) ptx::mbar_arrive_expect_tx(full + stage, (uint32_t)(kG * (kABytes + n * kSlab)));
           const int kx = k * kSlab;
+          uint8_t* sx = st + kABytes;
+          // rows in the fewest boxes, each map at a fixed parameter address
+          auto rows = [&](auto load) {
+            int r = 0;
+            if (F::kBRows >= 128 && n & 128) { load(&p.tm_x[3], r); r += 128; }
+            if (n & 64) { load(&p.tm_x[2], r); r += 64; }
+            if (n & 32) { load(&p.tm_x[1], r); r += 32; }
+            if (n & 16) load(&p.tm_x[0], r);
+          };
           if constexpr (kG == 2) {
             const uint32_t fb = remote(full + stage, 0);
             ptx::tma_load_2d_pair(st, &p.tm_w, fb, kx, wrow);
             if (kUp) ptx::tma_load_2d_pair(st + 64 * kSlab, &p.tm_wu, fb, kx, wrow);
-            if (n == F::kBRows) {
-              ptx::tma_load_2d_pair(st + kABytes, &p.tm_x, fb, kx, xrow);
-            } else {
-              for (int r = 0; r < n; r += 16)
-                ptx::tma_load_2d_pair(st + kABytes + r * kSlab, &p.tm_x16, fb, kx, xrow + r);
-            }
+            rows([&](const CUtensorMap* m, int r) { ptx::tma_load_2d_pair(sx + r * kSlab, m, fb, kx, xrow + r); });
           } else {
             uint64_t* fb = full + stage;
             ptx::tma_load_2d_hint(st, &p.tm_w, fb, kx, wrow, pol);
             if (kUp) ptx::tma_load_2d_hint(st + 64 * kSlab, &p.tm_wu, fb, kx, wrow, pol);
-            if (n == F::kBRows) {
-              ptx::tma_load_2d(st + kABytes, &p.tm_x, fb, kx, xrow);
-            } else {
-              for (int r = 0; r < n; r += 16) ptx::tma_load_2d(st + kABytes + r * kSlab, &p.tm_x16, fb, kx, xrow + r);
-            }
+            rows([&](const CUtensorMap* m, int r) { ptx::tma_load_2d(sx + r * kSlab, m, fb, kx, xrow + r); });
           }
         }
         __syncwarp();
@@ -441,10 +445,10 @@ cudaError_t launch(const GemmI8Args& a) {
   memset(&p, 0, sizeof(p));
   const int64_t N = a.d.N, K = a.d.K, E = a.d.experts;
   if (!ffn::make_tmap(&p.tm_w, a.w, ffn::kElU8, K, E * N, kSlab, F::kCh) ||
-      (kUp && !ffn::make_tmap(&p.tm_wu, a.wu, ffn::kElU8, K, E * N, kSlab, F::kCh)) ||
-      !ffn::make_tmap(&p.tm_x, a.x, ffn::kElU8, K, a.d.M, kSlab, F::kBRows) ||
-      !ffn::make_tmap(&p.tm_x16, a.x, ffn::kElU8, K, a.d.M, kSlab, 16))
+      (kUp && !ffn::make_tmap(&p.tm_wu, a.wu, ffn::kElU8, K, E * N, kSlab, F::kCh)))
     return cudaErrorInvalidValue;
+  for (int b = 0; b < 4; ++b)
+    if (!ffn::make_tmap(&p.tm_x[b], a.x, ffn::kElU8, K, a.d.M, kSlab, 16 << b)) return cudaErrorInvalidValue;
   p.xs = a.xs;
   p.ws = a.ws;
   p.wus = a.wus;
