@@ -13,10 +13,15 @@
 //
 // Per CTA (320 threads): warp 0 streams K slabs of 128 bytes into a ring of
 // stages with TMA, warp 1 issues the MMAs into one of two accumulators, warps
-// 2-9 read the other one back, scale and store. Two forms:
-//   kG = 1  chunks of 64 rows, one CTA: a decode batch reads every weight once,
+// 2-9 read the other one back, scale and store. Three forms:
+//   kOne    chunks of 64 rows, one CTA: a decode batch reads every weight once,
 //           and the many small stages keep the loads in flight that HBM needs
-//   kG = 2  chunks of 256 rows, a CTA pair (M = 256 over two SMs, each holding
+//   kSplit  the same with a unit's K slabs split over the CTAs of a cluster,
+//           where there are fewer units than SMs: each CTA writes its int32
+//           sums of a row into the shared memory of the CTA that owns the row
+//           (row mod cluster size), which adds and stores them (integers: the
+//           order changes nothing)
+//   kPair   chunks of 256 rows, a CTA pair (M = 256 over two SMs, each holding
 //           half of the rows): for many rows an expert, where the tensor cores
 //           and the L2's delivery of operands bound it
 // Every wait is bounded: on expiry the kernel latches MOE_ERR_TIMEOUT, drains
@@ -24,6 +29,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "ffn_common.cuh"
 
@@ -40,13 +46,18 @@ constexpr int kEpiThreads = 256;
 constexpr int kMaxExperts = 1024;
 constexpr int kBand = 8;           // chunks that share each channel tile in turn (unit order)
 
-template <int kG, bool kUp>
+enum : int { kOne, kSplit, kPair };
+
+template <int kForm, bool kUp>
 struct Form {
+  static constexpr int kG = kForm == kPair ? 2 : 1;           // CTAs of one MMA
   static constexpr int kRows = kG == 2 ? 256 : 64;            // rows of a chunk: MMA columns
   static constexpr int kBRows = kRows / kG;                   // of them in this CTA's shared memory
   static constexpr int kCh = kUp ? 64 : 128;                  // channels a CTA
   static constexpr int kStage = kABytes + kBRows * kSlab;
-  static constexpr int kXchg = kUp ? 2 * 2 * 16 * 64 * 4 : 0; // [set][gate, up][16 rows][64 channels] int32
+  // kSplit: [CTA][rows owned][128 A rows] int32, the sums of this CTA's rows; else with up
+  // [set][gate, up][16 rows][64 channels] int32
+  static constexpr int kXchg = kForm == kSplit ? kRows * 128 * 4 : kUp ? 2 * 2 * 16 * 64 * 4 : 0;
   static constexpr int kXs = 2 * kRows * 4;                   // row scales, two units
   static constexpr int kTab = (kMaxExperts + 1) * 4 + 12;
   static constexpr int kCtl = 512;
@@ -57,7 +68,7 @@ struct Form {
   static constexpr int kOffCtl = (kOffTab + kTab + 15) / 16 * 16;
   static constexpr int kSmem = kOffCtl + kCtl + 1024;         // and alignment slack
   static constexpr uint32_t kTmemCols = 2 * kRows;
-  static_assert(kSmem <= kMaxDynSmem && (2 * kStages + 5) * 8 <= kCtl - 32, "shared memory");
+  static_assert(kSmem <= kMaxDynSmem && (2 * kStages + 7) * 8 <= kCtl - 32, "shared memory");
 };
 
 struct Params {
@@ -89,9 +100,10 @@ struct Unit {
   int64_t row;   // first row
 };
 
-template <int kG, bool kUp, typename O>
+template <int kForm, bool kUp, typename O>
 __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_constant__ Params p) {
-  using F = Form<kG, kUp>;
+  using F = Form<kForm, kUp>;
+  constexpr int kG = F::kG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* ctl = smem + F::kOffCtl;
@@ -100,14 +112,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
   uint64_t* acc_full = empty + F::kStages;                // [2] each CTA: an accumulator is complete
   uint64_t* acc_empty = acc_full + 2;                     // [2] CTA 0: all epilogue warps have read it
   uint64_t* drain = acc_empty + 2;
+  uint64_t* part_full = drain + 1;                        // kSplit: all CTAs' sums of this one's rows are here
+  uint64_t* part_free = part_full + 1;                    // kSplit: all CTAs have read what they got
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + F::kCtl - 32);
   volatile int* epi_ok = abort_flag + 1;                  // [2]
+  volatile int* part_ok = epi_ok + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctl + F::kCtl - 16);
   int* tab = reinterpret_cast<int*>(smem + F::kOffTab);   // [experts + 1] first chunk of each expert
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = kG == 2 ? ptx::cluster_ctarank() : 0u;
-  const int worker = blockIdx.x / kG, workers = gridDim.x / kG;
+  const uint32_t rank = kForm == kPair ? ptx::cluster_ctarank() : 0u;   // CTA of the MMA
+  const uint32_t part = kForm == kSplit ? ptx::cluster_ctarank() : 0u;  // share of K
+  const uint32_t parts = kForm == kSplit ? ptx::cluster_nctarank() : 1u;
+  const int team = kForm == kSplit ? (int)parts : kG;                   // CTAs of a worker
+  const int worker = blockIdx.x / team, workers = gridDim.x / team;
+  const int k_first = (int)(part * (uint32_t)p.nk / parts), k_end = (int)((part + 1) * (uint32_t)p.nk / parts);
   const int E = p.win.experts;
 
   if (threadIdx.x == 0) {
@@ -120,6 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
       ptx::mbar_init(acc_empty + s, 8 * kG);
     }
     ptx::mbar_init(drain, 1);
+    ptx::mbar_init(part_full, 8 * parts);
+    ptx::mbar_init(part_free, 8 * parts);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -149,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     if (lane == 0) tab[E] = first;
   }
   ptx::tc_fence_before();
-  if constexpr (kG == 2) ptx::cluster_sync();   // both CTAs' barriers and tensor memory exist
+  if constexpr (kForm != kOne) ptx::cluster_sync();   // every CTA's barriers and tensor memory exist
   else __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -199,14 +220,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     }
     uint32_t stage = 0, phase = 0;
     uint32_t armed = 0, armed_parity = 0;
-    const uint64_t pol = kG == 2 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
+    const uint64_t pol = ptx::policy_evict_first();   // kOne, kSplit: weights are read once
     bool ok = true;
     for (int u = worker; ok && u < units; u += workers) {
       const Unit j = unit(u);
       const int n = columns(j.rows) / kG;                       // rows this CTA loads
       const int wrow = (int)(j.e * p.N + (int64_t)j.tile * (kG * F::kCh) + rank * F::kCh);
       const int xrow = (int)(j.row + rank * n);
-      for (int k = 0; k < p.nk; ++k) {
+      for (int k = k_first; k < k_end; ++k) {
         int good = 1;
         if (lane == 0) good = wait_bar(empty + stage, phase ^ 1u, abort_flag, p.hdr, 0x48000000u | stage);
         if (!__shfl_sync(0xffffffffu, good, 0)) { ok = false; break; }
@@ -265,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
         ptx::tc_fence_after();
         const uint32_t d = tmem + slot * F::kRows;
         const uint32_t idesc = ptx::idesc_i8(128 * kG, columns(unit(u).rows));
-        for (int k = 0; k < p.nk; ++k) {
+        for (int k = k_first; k < k_end; ++k) {
           if (lane == 0) good = wait_bar(full + stage, phase, abort_flag, p.hdr, 0x68000000u | stage);
           if (!__shfl_sync(0xffffffffu, good, 0)) { ok = false; break; }
           ptx::tc_fence_after();
@@ -274,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
           if (ptx::elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {   // 32 bytes of K per MMA
-              if constexpr (kG == 2) ptx::mma_i8_pair(d, a + 2 * kk, b + 2 * kk, idesc, (k | kk) ? 1u : 0u);
-              else ptx::mma_i8(d, a + 2 * kk, b + 2 * kk, idesc, (k | kk) ? 1u : 0u);
+              if constexpr (kG == 2) ptx::mma_i8_pair(d, a + 2 * kk, b + 2 * kk, idesc, k > k_first || kk ? 1u : 0u);
+              else ptx::mma_i8(d, a + 2 * kk, b + 2 * kk, idesc, k > k_first || kk ? 1u : 0u);
             }
             if constexpr (kG == 2) {
               ptx::mma_commit_pair(remote(empty + stage, 0));
@@ -317,10 +338,81 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     int* xg = reinterpret_cast<int*>(smem + F::kOffXchg) + set * 2 * 16 * 64;   // [16][64]
     int* xu = xg + 16 * 64;
     float* xs_all = reinterpret_cast<float*>(smem + F::kOffXs);
+    // kSplit: this CTA's sums to the owners of their rows, then its own rows
+    auto split_epilogue = [&](const Unit& j, uint32_t slot, uint32_t use, uint32_t turn) -> bool {
+      int* sums = reinterpret_cast<int*>(smem + F::kOffXchg);
+      const int shift = __ffs(parts) - 1, owned = F::kRows >> shift;   // parts is a power of two
+      // a thread's channel when it stores, fetched while the sums are made
+      const int n = et % F::kCh;
+      const int64_t nn = (int64_t)j.tile * F::kCh + n;
+      const bool real = nn < p.N;
+      const float sw = real ? __ldg(p.ws + j.e * p.N + nn) : 0.f;
+      const float su = kUp && real ? __ldg(p.wus + j.e * p.N + nn) : 0.f;
+      float* xs = xs_all + slot * F::kRows;
+      if (et < j.rows) xs[et] = __ldg(p.xs + j.row + et);
+      if (et == 0)
+        epi_ok[slot] = wait_bar(acc_full + slot, use, abort_flag, p.hdr, 0x78000000u | slot) &&
+                       wait_bar<true>(part_free, turn ^ 1u, abort_flag, p.hdr, 0x79000000u);
+      ptx::named_barrier(1, kEpiThreads);
+      if (!epi_ok[slot]) return false;
+      while (!ptx::mbar_try_wait(acc_full + slot, use)) {}   // both completed: return at once
+      while (!ptx::mbar_try_wait_cluster(part_free, turn ^ 1u)) {}
+      ptx::tc_fence_after();
+      for (int c0 = 32 * set; c0 < j.rows; c0 += 64) {
+        uint32_t v[32];
+        ptx::tmem_ld_x32(tmem + slot * F::kRows + ((uint32_t)(q * 32) << 16) + c0, v);
+        ptx::tmem_wait_ld();
+        int* mine = sums + (part * owned + (c0 >> shift)) * 128 + arow;
+        auto push = [&](auto count) {   // column c to owner c mod kParts
+          constexpr int kParts = decltype(count)::value;
+          uint32_t at[kParts];
+#pragma unroll
+          for (int r = 0; r < kParts; ++r) at[r] = remote(mine, r);
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < j.rows) ptx::st_cluster_u32(at[c % kParts] + c / kParts * 512, v[c]);
+        };
+        if (parts == 2) push(std::integral_constant<int, 2>());
+        else push(std::integral_constant<int, 4>());
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(acc_empty + slot);
+        for (uint32_t r = 0; r < parts; ++r) ptx::mbar_arrive_cluster(remote(part_full, r));
+      }
+      if (et == 0) *part_ok = wait_bar<true>(part_full, turn, abort_flag, p.hdr, 0x7a000000u);
+      ptx::named_barrier(1, kEpiThreads);
+      if (!*part_ok) return false;
+      while (!ptx::mbar_try_wait_cluster(part_full, turn)) {}   // completed: returns at once
+      if (real) {
+        for (int o = et / F::kCh; (o << shift) + (int)part < j.rows; o += kEpiThreads / F::kCh) {
+          const int c = (o << shift) + (int)part;
+          int a = 0, b = 0;
+          for (uint32_t r = 0; r < parts; ++r) {
+            a += sums[(r * owned + o) * 128 + n];
+            if (kUp) b += sums[(r * owned + o) * 128 + 64 + n];
+          }
+          float f = (float)a * sw * xs[c];
+          if (kUp) f = (sizeof(O) == 2 ? quick_silu(f) : f / (1.f + expf(-f))) * ((float)b * su * xs[c]);
+          O* y = reinterpret_cast<O*>(p.y) + (j.row + c) * p.N + nn;
+          if constexpr (sizeof(O) == 2) *y = __float2bfloat16_rn(f);
+          else *y = f;
+        }
+      }
+      __syncwarp();
+      if (lane == 0)
+        for (uint32_t r = 0; r < parts; ++r) ptx::mbar_arrive_cluster(remote(part_free, r));
+      return true;
+    };
     uint32_t i = 0;
     for (int u = worker; u < units; u += workers, ++i) {
       const Unit j = unit(u);
       const uint32_t slot = i & 1u, use = (i >> 1) & 1u;
+      if constexpr (kForm == kSplit) {
+        if (!split_epilogue(j, slot, use, i & 1u)) break;
+        continue;
+      }
       float* xs = xs_all + slot * F::kRows;
       const int64_t n0 = (int64_t)j.tile * (kG * F::kCh) + rank * F::kCh + ch;
       const bool real = n0 < p.N;
@@ -418,9 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
       }
     }
   }
-  // every role is done in both CTAs before tensor memory is freed
+  // every role is done in every CTA before tensor memory is freed and one exits
   ptx::tc_fence_before();
-  if constexpr (kG == 2) ptx::cluster_sync();
+  if constexpr (kForm != kOne) ptx::cluster_sync();
   else __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
@@ -431,11 +523,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
 
 // ---- host side ------------------------------------------------------------
 
-template <int kG, bool kUp, typename O>
-cudaError_t launch(const GemmI8Args& a) {
-  using F = Form<kG, kUp>;
+// team: CTAs of a worker (the cluster), 1, 2 or 4
+template <int kForm, bool kUp, typename O>
+cudaError_t launch(const GemmI8Args& a, int team) {
+  using F = Form<kForm, kUp>;
   constexpr int kMaxDevices = 64;
-  static std::atomic<int> resident[kMaxDevices];   // clusters at once on each device, 0 = not asked yet
+  static std::atomic<int> resident[kMaxDevices][3];   // clusters of 1, 2, 4 at once on each device, 0 = not asked yet
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -458,52 +551,62 @@ cudaError_t launch(const GemmI8Args& a) {
   p.M = a.d.M;
   p.N = N;
   p.nk = (int)ceil_div(K, kSlab);
-  p.tiles = (int)ceil_div(N, kG * F::kCh);
+  p.tiles = (int)ceil_div(N, F::kG * F::kCh);
 
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kG;
+  attr[0].val.clusterDim.x = (unsigned)team;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)(kG * std::max(1, a.num_sms / kG)), 1, 1);
+  const int fit = std::max(1, a.num_sms / team);
+  cfg.gridDim = dim3((unsigned)(team * fit), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = F::kSmem;
   cfg.stream = a.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int workers = resident[dev].load(std::memory_order_acquire);
+  std::atomic<int>& known = resident[dev][team == 1 ? 0 : team == 2 ? 1 : 2];
+  int workers = known.load(std::memory_order_acquire);
   if (workers == 0) {
-    if ((err = cudaFuncSetAttribute(gemm_i8_kernel<kG, kUp, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if ((err = cudaFuncSetAttribute(gemm_i8_kernel<kForm, kUp, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     F::kSmem)) != cudaSuccess)
       return err;
-    if (cudaOccupancyMaxActiveClusters(&workers, gemm_i8_kernel<kG, kUp, O>, &cfg) != cudaSuccess || workers < 1)
-      workers = std::max(1, a.num_sms / kG);
+    if (cudaOccupancyMaxActiveClusters(&workers, gemm_i8_kernel<kForm, kUp, O>, &cfg) != cudaSuccess || workers < 1)
+      workers = fit;
     (void)cudaGetLastError();   // a failed query is not the launch's error
-    resident[dev].store(workers, std::memory_order_release);
+    known.store(workers, std::memory_order_release);
   }
   // no more workers than the most units there can be
   const int64_t most = (ceil_div(a.d.M, F::kRows) + (a.win.offsets ? E : 0)) * p.tiles;
-  cfg.gridDim.x = (unsigned)(kG * std::min<int64_t>(std::min(workers, std::max(1, a.num_sms / kG)), most));
-  return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<kG, kUp, O>, p);
+  cfg.gridDim.x = (unsigned)(team * std::min<int64_t>(std::min(workers, fit), most));
+  return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<kForm, kUp, O>, p);
 }
 
-template <int kG, bool kUp>
-cudaError_t launch_out(const GemmI8Args& a) {
-  return a.d.out_dtype == MOE_F32 ? launch<kG, kUp, float>(a) : launch<kG, kUp, __nv_bfloat16>(a);
-}
-
-template <int kG>
-cudaError_t launch_form(const GemmI8Args& a) {
-  return a.wu ? launch_out<kG, true>(a) : launch_out<kG, false>(a);
+template <int kForm>
+cudaError_t launch_form(const GemmI8Args& a, int team) {
+  const bool f32 = a.d.out_dtype == MOE_F32;
+  if (a.wu) return f32 ? launch<kForm, true, float>(a, team) : launch<kForm, true, __nv_bfloat16>(a, team);
+  return f32 ? launch<kForm, false, float>(a, team) : launch<kForm, false, __nv_bfloat16>(a, team);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_i8(const GemmI8Args& a) {
-  const int64_t fill = a.d.fill > 0 && a.d.fill < a.d.M ? a.d.fill : a.d.M;
-  return fill > 64 * a.d.experts && a.num_sms >= 2 ? launch_form<2>(a) : launch_form<1>(a);
+  const int64_t fill = a.d.fill > 0 && a.d.fill < a.d.M ? a.d.fill : a.d.M, E = a.d.experts;
+  const int64_t nk = ceil_div(a.d.K, kSlab), ch = a.wu ? 64 : 128;
+  // units to expect: experts with rows, each of its share
+  const int64_t used = std::min(E, fill), share = ceil_div(fill, used);
+  const int64_t pairs = used * ceil_div(share, 256) * ceil_div(a.d.N, 2 * ch);
+  if (share > 64 && 2 * pairs >= a.num_sms / 2 && a.num_sms >= 2) return launch_form<kPair>(a, 2);
+  const int64_t ones = used * ceil_div(share, 64) * ceil_div(a.d.N, ch);
+  // A CTA takes 0.24 us a slab; sharing K over 2 or 4 costs 2 to 4 us. Measured,
+  // 1 / 2 / 4 CTAs: one row, 4096 x 7168 17.2 / 12.3 / 9.9 us, 64 rows 18.0 /
+  // 15.1 / 12.0; 7168 x 2048 7.6 / 7.6 us, 64 rows 8.2 / 10.2
+  int team = 1;
+  while (team < 4 && ones * 2 * team <= a.num_sms && nk >= 24 * team) team *= 2;
+  return team > 1 ? launch_form<kSplit>(a, team) : launch_form<kOne>(a, 1);
 }
 
 }  // namespace moe
