@@ -599,8 +599,12 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a) {
   // units to expect: experts with rows, each of its share
   const int64_t used = std::min(E, fill), share = ceil_div(fill, used);
   const int64_t pairs = used * ceil_div(share, 256) * ceil_div(a.d.N, 2 * ch);
-  if (share > 64 && 2 * pairs >= a.num_sms / 2 && a.num_sms >= 2) return launch_form<kPair>(a, 2);
   const int64_t ones = used * ceil_div(share, 64) * ceil_div(a.d.N, ch);
+  // A pair takes 0.36 us a slab (a full chunk), a CTA 0.24 us: compare the
+  // rounds of units. Measured, pairs / single CTAs: 200 x 4096 x 7168 28 / 18 us;
+  // 32 experts of gate/up 2048 x 7168, 64 rows each 180 / 164 us, 128 rows 186 / 234
+  if (a.num_sms >= 2 && 3 * ceil_div(pairs, a.num_sms / 2) <= 2 * ceil_div(ones, a.num_sms))
+    return launch_form<kPair>(a, 2);
   // A CTA takes 0.24 us a slab; sharing K over 2 or 4 costs 2 to 4 us. Measured,
   // 1 / 2 / 4 CTAs: one row, 4096 x 7168 17.2 / 12.3 / 9.9 us, 64 rows 18.0 /
   // 15.1 / 12.0; 7168 x 2048 7.6 / 7.6 us, 64 rows 8.2 / 10.2
