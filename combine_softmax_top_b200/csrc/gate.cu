@@ -435,12 +435,11 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
   sort_descending<0, NV>(key);
   uint32_t won = kNoKey;   // lane j: slot j's key (lane k: that of the best one left)
   auto pop = [&](uint32_t m, int j) {   // the largest head m, into lane j
-    if (li == j) won = m;
-    if (key[0] == m) {
+    won = li == j ? m : won;
+    const bool win = key[0] == m;
 #pragma unroll
-      for (int v = 0; v + 1 < NV; ++v) key[v] = key[v + 1];
-      key[NV - 1] = kNoKey;
-    }
+    for (int v = 0; v + 1 < NV; ++v) key[v] = win ? key[v + 1] : key[v];
+    key[NV - 1] = win ? kNoKey : key[NV - 1];
   };
   const int rounds = lossless ? k : min(k + 1, S);
 #pragma unroll 1
@@ -467,7 +466,9 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
       uint32_t m = sub_max<S>(key[0]);
       auto reaches = [&]() { return doubt && m != kNoKey && (m | kIdx) >= lim; };
       while (__any_sync(kFull, reaches() && n < S)) {
-        if (reaches() && n < S) pop(m, n++);
+        const bool take = reaches() && n < S;
+        pop(take ? m : ~0u, take ? n : -1);   // ~0 is no key: nothing is taken
+        n += take;
         m = sub_max<S>(key[0]);
       }
       unsure = unsure || reaches();   // more candidates than lanes
