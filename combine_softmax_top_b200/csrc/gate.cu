@@ -32,7 +32,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr uint32_t kNoKey = 0u;   // below the key of every number
+constexpr uint32_t kNoKey = 0u;
+constexpr uint32_t kLeastKey = 0x00800000u;   // of the lowest number; -infinity's is below
 
 // 32-bit key that orders like the number
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -324,18 +325,22 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     for (int v = 0; v < NV; ++v) l[v] = c[v] = 0.f;
     if (li == 0 && mine_to_store) latch_error(hdr, MOE_ERR_NONFINITE, (uint32_t)t);
   }
+  if (!wide) {   // slots without an expert stay below all others
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (v >= mine) l[v] = c[v] = -INFINITY;
+  }
   const bool lossless = sizeof(T) == 2 && !bias;   // the keys tell all choice values apart
   const bool scores = bias || (g.groups > 1 && g.group_best == 2);
   float top = 0.f, z = 1.f, inv_z = 1.f;
   if (!kSigmoid && (scores || !renorm)) {
     top = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      if (v < mine) top = fmaxf(top, l[v]);
+    for (int v = 0; v < NV; ++v) top = fmaxf(top, l[v]);
     top = sub_max<S>(top);
     float part = 0.f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) part += v < mine ? quick_exp(l[v] - top) : 0.f;
+    for (int v = 0; v < NV; ++v) part += quick_exp(l[v] - top);
     z = sub_sum<S>(part);
     inv_z = 1.f / z;
   }
@@ -356,8 +361,7 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     for (int v = 0; v < NV; ++v) c[v] = l[v];
   }
 
-  // groups: which slots' groups are open, one bit each
-  uint32_t open = ~0u;
+  // groups: the slots of closed ones go below all others
   bool unsure = false;
   if (g.groups > 1) {
     float b1 = -INFINITY, b2 = -INFINITY;
@@ -369,8 +373,7 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     if (gr.span) {   // a group is an aligned set of lanes, all of them full
       gi = li >> (__ffs(gr.span) - 1);
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (v < mine) take(c[v]);
+      for (int v = 0; v < NV; ++v) take(c[v]);
       for (int off = 1; off < gr.span; off <<= 1) {
         const float o1 = __shfl_xor_sync(kFull, b1, off), o2 = __shfl_xor_sync(kFull, b2, off);
         b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
@@ -411,27 +414,27 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     const bool in = gi < g.groups;
     unsure = in && may >= g.topk_groups && above < g.topk_groups;
     const uint32_t opens = __ballot_sync(kFull, in && may < g.topk_groups) >> base;
-    if (gr.span) {
-      open = may < g.topk_groups ? ~0u : 0u;
-    } else {
-      open = 0;
-      int q = e0 / gr.n, at = e0 - q * gr.n;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        if (v < mine) open |= ((opens >> q) & 1u) << v;
-        if (++at == gr.n) { at = 0; ++q; }
-      }
-    }
     if (!bias && scores) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) c[v] = l[v];   // the scores only ranked the groups
+    }
+    if (gr.span) {
+      const bool open = may < g.topk_groups;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) c[v] = open ? c[v] : -INFINITY;
+    } else {
+      int q = e0 / gr.n, at = e0 - q * gr.n;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if (v < mine && !((opens >> q) & 1u)) c[v] = -INFINITY;
+        if (++at == gr.n) { at = 0; ++q; }
+      }
     }
   }
 
   uint32_t key[NV];
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
-    key[v] = v < mine && ((open >> v) & 1u) ? (order_key(c[v]) & ~kIdx) | (kIdx - (uint32_t)(e0 + v)) : kNoKey;
+  for (int v = 0; v < NV; ++v) key[v] = (order_key(c[v]) & ~kIdx) | (kIdx - (uint32_t)(e0 + v));
   sort_descending<0, NV>(key);
   uint32_t won = kNoKey;   // lane j: slot j's key (lane k: that of the best one left)
   auto pop = [&](uint32_t m, int j) {   // the largest head m, into lane j
@@ -444,7 +447,7 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
   const int rounds = lossless ? k : min(k + 1, S);
 #pragma unroll 1
   for (int j = 0; j < rounds; ++j) pop(sub_max<S>(key[0]), j);
-  int sel = won == kNoKey ? -1 : (int)(kIdx - (won & kIdx));
+  int sel = won < kLeastKey ? -1 : (int)(kIdx - (won & kIdx));
   float lj = sel >= 0 ? load_logit(row + sel) : 0.f;
   unsure = sub_any<S>(unsure) && !dead;   // which groups are open
   if (!lossless) {
@@ -464,7 +467,7 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
       const uint32_t lim = order_key(__shfl_sync(kFull, v - (near + cut), base + k - 1));
       int n = rounds;
       uint32_t m = sub_max<S>(key[0]);
-      auto reaches = [&]() { return doubt && m != kNoKey && (m | kIdx) >= lim; };
+      auto reaches = [&]() { return doubt && m >= kLeastKey && (m | kIdx) >= lim; };
       while (__any_sync(kFull, reaches() && n < S)) {
         const bool take = reaches() && n < S;
         pop(take ? m : ~0u, take ? n : -1);   // ~0 is no key: nothing is taken
@@ -472,7 +475,7 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
         m = sub_max<S>(key[0]);
       }
       unsure = unsure || reaches();   // more candidates than lanes
-      const int cand = won == kNoKey ? -1 : (int)(kIdx - (won & kIdx));
+      const int cand = won < kLeastKey ? -1 : (int)(kIdx - (won & kIdx));
       double zd = 1.0;
       if (!kSigmoid && bias) {
         double part = 0.0;
