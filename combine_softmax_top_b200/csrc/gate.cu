@@ -133,27 +133,18 @@ __device__ __forceinline__ bool sub_any(bool p) {
   return ((all >> ((threadIdx.x & 31) / S * S)) & ((1u << (S & 31)) - 1u)) != 0u;
 }
 
-// exp for the choice: off by (2 + 1.173 |x|) 2^-23 relative at most
+// exp for the choice: off by (4 + 1.5 |x|) 2^-24 relative at most (ex2.approx:
+// 2^-22; its argument is rounded twice, 2^-24 |x| / ln 2 each with a factor ln 2)
 __device__ __forceinline__ float quick_exp(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
   return r;
 }
-// 1 / x, x >= 1 (0 for infinity): off by 2^-22 relative at most
+// 1 / x, x >= 1 (0 for infinity): off by 2^-23 relative at most
 __device__ __forceinline__ float quick_rcp(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
-}
-
-// The warp's best (value, index): larger value, lower index on a tie.
-__device__ __forceinline__ void warp_best(double& v, int& i) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const double ov = __shfl_xor_sync(kFull, v, off);
-    const int oi = __shfl_xor_sync(kFull, i, off);
-    if (ov > v || (ov == v && oi < i)) { v = ov; i = oi; }
-  }
 }
 
 // Terms a_j of the chosen scores (lane j holds logit l of slot j, `live` if it
@@ -170,61 +161,78 @@ __device__ __forceinline__ float renorm_term(float l, bool live) {
   return l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - m) / (1.f + expf(l));
 }
 
-// The choice in binary64, lane j < k returning slot j's expert. c: E doubles
-// of shared memory of this warp.
+// 64-bit key that orders like the number
+__device__ __forceinline__ uint64_t order_key(double f) {
+  const uint64_t b = (uint64_t)__double_as_longlong(f + 0.0);
+  return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+
+// The choice in binary64, lane j < k returning slot j's expert. n: experts of a
+// group. c: E doubles of shared memory of this warp.
 template <typename T, bool kSigmoid>
-__device__ __noinline__ int choose_exactly(const T* row, const float* bias, int E, int k, moe_gate_desc g, float top,
-                                           double* c) {
+__device__ __noinline__ int choose_exactly(const T* row, const float* bias, int E, int k, int n, moe_gate_desc g,
+                                           float top, double* c) {
   const int lane = threadIdx.x & 31;
+  const bool ranks = g.groups > 1 && g.group_best == 2;   // groups are ranked by scores
   double z = 1.0;
-  if (!kSigmoid) {
+  if (!kSigmoid && (bias || ranks)) {
     z = 0.0;
     for (int e = lane; e < E; e += 32) z += exp((double)load_logit(row + e) - (double)top);
     z = sub_sum<32>(z);
   }
-  auto score = [&](int e) -> double {
+  for (int e = lane; e < E; e += 32) {
     const double l = load_logit(row + e);
-    return kSigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / z;
-  };
-  for (int e = lane; e < E; e += 32) c[e] = bias ? score(e) + (double)bias[e] : (double)load_logit(row + e);
-  __syncwarp();
-  if (g.groups > 1) {
-    const int n = E / g.groups;
-    double rank = -INFINITY;
-    if (lane < g.groups) {
-      double b1 = -INFINITY, b2 = -INFINITY;
-      for (int i = 0; i < n; ++i) {
-        const int e = lane * n + i;
-        const double v = (!bias && g.group_best == 2) ? score(e) : c[e];
-        if (v > b1) { b2 = b1; b1 = v; }
-        else if (v > b2) b2 = v;
-      }
-      rank = g.group_best == 2 ? b1 + b2 : b1;
-    }
-    uint32_t open = 0;
-    for (int j = 0; j < g.topk_groups; ++j) {
-      const bool free = lane < g.groups && !((open >> lane) & 1u);
-      double v = free ? rank : -INFINITY;
-      int i = free ? lane : 64;
-      warp_best(v, i);
-      open |= 1u << i;
-    }
-    __syncwarp();
-    for (int e = lane; e < E; e += 32)
-      if (!((open >> (e / n)) & 1u)) c[e] = -INFINITY;
-    __syncwarp();
+    const double s = !bias && !ranks ? l : kSigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / z;
+    c[e] = bias ? s + (double)bias[e] : s;
   }
+  __syncwarp();
+  uint32_t open = kFull;
+  if (g.groups > 1) {
+    double b1 = -INFINITY, b2 = -INFINITY;
+    if (lane < g.groups) {
+      for (int i = 0; i < n; ++i) {
+        const double v = c[lane * n + i];
+        b2 = fmax(b2, fmin(b1, v));
+        b1 = fmax(b1, v);
+      }
+    }
+    const double r = g.group_best == 2 ? b1 + b2 : b1;
+    int above = 0;
+    for (int h = 0; h < g.groups; ++h) {
+      const double o = __shfl_sync(kFull, r, h);
+      above += o > r || (o == r && h < lane);
+    }
+    open = __ballot_sync(kFull, lane < g.groups && above < g.topk_groups);
+    __syncwarp();
+    for (int e = lane; e < E; e += 32) {   // each lane's own elements from here on
+      if (!((open >> (e / n)) & 1u)) c[e] = -INFINITY;
+      else if (ranks && !bias) c[e] = load_logit(row + e);
+    }
+  }
+  uint64_t best;
+  int who;
+  auto look = [&]() {   // this lane's largest, the lowest index of equals
+    best = 0;
+    who = INT32_MAX;
+    for (int e = lane; e < E; e += 32) {
+      const uint64_t q = order_key(c[e]);
+      if (q > best) { best = q; who = e; }
+    }
+  };
+  look();
   int sel = 0;
   for (int j = 0; j < k; ++j) {
-    double v = -INFINITY;
-    int i = INT32_MAX;
-    for (int e = lane; e < E; e += 32)
-      if (c[e] > v) { v = c[e]; i = e; }
-    warp_best(v, i);
-    if (lane == j) sel = i;
-    if (lane == 0) c[i] = -INFINITY;
-    __syncwarp();
+    const uint32_t hi = __reduce_max_sync(kFull, (uint32_t)(best >> 32));
+    const bool in = (uint32_t)(best >> 32) == hi;
+    const uint32_t lo = __reduce_max_sync(kFull, in ? (uint32_t)best : 0u);
+    const int e = (int)__reduce_min_sync(kFull, in && (uint32_t)best == lo ? (uint32_t)who : 0xFFFFFFFFu);
+    if (lane == j) sel = e;
+    if (who == e) {
+      c[e] = -INFINITY;
+      look();
+    }
   }
+  __syncwarp();
   return sel;
 }
 
@@ -345,13 +353,14 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     inv_z = 1.f / z;
   }
   // err0 + err1 |c|: how far c can be from its binary64 value, with exp off by
-  // (2 + 1.173 |x|) 2^-23 relative and the fast quotient by 2^-22.
-  // Sigmoid: s (1 - s) times the former is below 2^-23, the sum adds 2^-24, the
-  // quotient 2^-22. Softmax: x is itself off by |x| 2^-24; over z the errors of
-  // exp average to at most 10.5 * 2^-23 (of 1024 terms), and the sum has a
-  // depth of at most 37: below 2^-17 of the largest score 1 / z in all. The
-  // sum with the bias: 2^-24 |c|.
-  const float err0 = scores ? (kSigmoid ? 0x1p-21f : 0x1p-17f * inv_z) : 0.f;
+  // (4 + 1.5 |x|) 2^-24 relative (ex2 and the rounding of its argument) and the
+  // reciprocal by 2^-23.
+  // Sigmoid: s (1 - s) times the former is below 1.6 * 2^-24, the sum adds
+  // 2^-24, the reciprocal 2^-23: 4.6 * 2^-24. Softmax: over z the errors of exp
+  // average to at most 10.5 * 2^-23 (of 1024 terms), and the sum has a depth of
+  // at most 37: below 2^-17 of the largest score 1 / z in all. The sum with the
+  // bias: 2^-24 |c|.
+  const float err0 = scores ? (kSigmoid ? 5.f * 0x1p-24f : 0x1p-17f * inv_z) : 0.f;
   const float err1 = bias ? 0x1p-23f : 0.f;
   if (scores) {
 #pragma unroll
@@ -507,8 +516,8 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     const int src = __ffs(again) - 1, first = src - src % S;
     again &= ~((S == 32 ? kFull : (1u << (S & 31)) - 1u) << first);
     __syncwarp();
-    const int s = choose_exactly<T, kSigmoid>(logits + (int64_t)__shfl_sync(kFull, t, first) * E, bias, E, k, g,
-                                              __shfl_sync(kFull, top, first), scratch);
+    const int s = choose_exactly<T, kSigmoid>(logits + (int64_t)__shfl_sync(kFull, t, first) * E, bias, E, k, gr.n,
+                                              g, __shfl_sync(kFull, top, first), scratch);
     const int got = __shfl_sync(kFull, s, li);
     if (base == first && li < k) sel = got;
     __syncwarp();
