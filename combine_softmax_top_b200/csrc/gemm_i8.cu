@@ -153,22 +153,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
       ptx::tmem_relinquish();
     }
   }
-  if (warp == 2) {   // first chunk of every expert
-    int first = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      int64_t row0;
-      const int n = e0 + lane < E ? (window_rows(p.win, e0 + lane, p.M, &row0) + F::kRows - 1) / F::kRows : 0;
-      int inc = n;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += v;
-      }
-      if (e0 + lane < E) tab[e0 + lane] = first + inc - n;
-      first += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) tab[E] = first;
-  }
+  if (warp == 2)   // first chunk of every expert
+    window_prefix(p.win, p.M, (p.M + F::kRows - 1) / F::kRows + E, [](int n) { return (n + F::kRows - 1) / F::kRows; },
+                  tab);
   ptx::tc_fence_before();
   if constexpr (kForm != kOne) ptx::cluster_sync();   // every CTA's barriers and tensor memory exist
   else __syncthreads();

@@ -369,6 +369,34 @@ __device__ __forceinline__ int window_rows(const RowWindows& w, int e, int64_t M
   return n <= 0 ? 0 : (int)(n < M - o ? n : M - o);
 }
 
+// first[e] = units of the windows before e, first[experts] = their total, for
+// windows of units(rows) each, by one warp. Windows that do not overlap have at
+// most `limit` units; where there are more, the windows from there on count as
+// empty, so that no total overflows.
+template <typename F>
+__device__ __forceinline__ void window_prefix(const RowWindows& w, int64_t M, int64_t limit, F units, int* first) {
+  const int lane = threadIdx.x & 31;
+  int64_t at = 0;
+  bool over = false;
+  for (int e0 = 0; e0 < w.experts; e0 += 32) {
+    int64_t row0;
+    const int64_t n = !over && e0 + lane < w.experts ? units(window_rows(w, e0 + lane, M, &row0)) : 0;
+    int64_t inc = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += v;
+    }
+    const uint32_t fits = __ballot_sync(0xffffffffu, at + inc <= limit);   // sums grow: the lowest lanes
+    const int64_t end = __shfl_sync(0xffffffffu, at + inc, fits ? 31 - __clz(fits) : 0);
+    const int64_t last = fits ? end : at;
+    if (e0 + lane < w.experts) first[e0 + lane] = (int)((fits >> lane) & 1u ? at + inc - n : last);
+    at = last;
+    over = over || fits != 0xffffffffu;
+  }
+  if (lane == 0) first[w.experts] = (int)at;
+}
+
 cudaError_t launch_quant_i8(int64_t rows, int64_t cols, int32_t dtype, const void* x, const RowWindows& win,
                             int8_t* q, float* scale, int num_sms, cudaStream_t stream);
 

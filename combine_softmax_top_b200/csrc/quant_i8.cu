@@ -84,22 +84,8 @@ quant_i8_kernel(const T* __restrict__ x, int64_t rows, int cols, RowWindows win,
   const int tid = threadIdx.x % kTeam, lane = threadIdx.x & 31;
   int total = (int)rows;
   if (win.offsets) {
-    if (threadIdx.x < 32) {
-      int at = 0;
-      for (int e0 = 0; e0 < win.experts; e0 += 32) {
-        int64_t row0;
-        const int n = e0 + lane < win.experts ? window_rows(win, e0 + lane, rows, &row0) : 0;
-        int inc = n;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, inc, off);
-          if (lane >= off) inc += v;
-        }
-        if (e0 + lane < win.experts) first[e0 + lane] = at + inc - n;
-        at += __shfl_sync(0xffffffffu, inc, 31);
-      }
-      if (lane == 0) first[win.experts] = at;
-    }
+    if (threadIdx.x < 32)
+      window_prefix(win, rows, rows, [](int n) { return n; }, first);
     __syncthreads();
     total = first[win.experts];
   }

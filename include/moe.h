@@ -488,8 +488,9 @@ MOE_API moe_status moe_gate_backward(const moe_shape* shape, const moe_gate_desc
  * on int8 rows (one scale per token), the W8A8 form of a checkpoint. Rows can
  * be all of a matrix, or only the filled rows of `experts` windows: window e
  * is rows offsets[e] .. offsets[e] + counts[e] - 1, as moe_dispatch lays them
- * out (moe_dispatch_bufs). Windows must not overlap; what a window holds
- * past the last of the M rows (or of a negative offset) is not worked on.
+ * out (moe_dispatch_bufs). Windows must not overlap (rows of windows that do
+ * have unspecified results, other rows keep theirs); what a window holds past
+ * the last of the M rows (or of a negative offset) is not worked on.
  * Other rows are neither read into a result nor written. These are serving
  * calls: integers have no gradient.
  *

@@ -7,6 +7,10 @@ rounding to bf16 2^-8 more. silu(g) u = g u / (1 + exp(-g)): g and u carry
 3 * 2^-24 each, which silu amplifies by at most 1 + |g|; exp, the sum, the
 quotient and the product add 2 * 2^-23 + 3 * 2^-24: (3 (1 + |g|) + 10) 2^-24.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -271,6 +275,30 @@ def test_windows_out_of_range_are_cut(ws):
     close(y[150:], *gemm_ref(x[150:], xs[150:], w[1], wsc[1]), "f32", False)
 
 
+def test_overlapping_windows_stay_in_bounds(ws):
+    """Windows that overlap have unspecified rows, and nothing else changes:
+    1024 windows over the same rows have more units than any that do not."""
+    M, N, K, E = 3000, 8, 32, 1024
+    x, xs = ints((M, K), 1).cuda(), torch.ones(M, device="cuda")
+    w, wsc = ints((E, N, K), 3).cuda(), torch.ones(E, N, device="cuda")
+    o = torch.full((E,), 100, dtype=torch.int32, device="cuda")
+    c = torch.full((E,), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    for fill in (0, 1):
+        y = torch.full((M, N), 77.0, device="cuda")
+        moe.moe_gemm_i8(x, xs, w, wsc, y, ws, offsets=o, counts=c, fill=fill)
+        assert moe.moe_poll_status(ws) == 0
+        assert bool((y[:100] == 77).all())
+    q, s = run_quant(torch.randn(M, 64, device="cuda"), offsets=o, counts=c)
+    assert (q[:100] == 99).all() and (s[:100] == -5).all()
+    # a second window repeats the first: the same weights give the same rows twice
+    o = torch.tensor([100, 100], dtype=torch.int32, device="cuda")
+    c = torch.tensor([1000, 1000], dtype=torch.int32, device="cuda")
+    y = torch.full((M, N), 77.0, device="cuda")
+    moe.moe_gemm_i8(x, xs, w[:1].expand(2, N, K).contiguous(), wsc[:2], y, ws, offsets=o, counts=c)
+    close(y[100:1100], *gemm_ref(x[100:1100].cpu(), torch.ones(1000), w[0].cpu(), torch.ones(N)), "f32", False)
+    assert bool((y[1100:] == 77).all())
+
+
 def test_nan_scale_reaches_its_row_only(ws):
     x, w = ints((5, 64), 1).cuda(), ints((9, 64), 2).cuda()
     xs, wsc = torch.ones(5, device="cuda"), torch.ones(9, device="cuda")
@@ -337,6 +365,41 @@ def test_streams_graphs_and_two_calls_at_once(ws):
         torch.cuda.synchronize()
         assert torch.equal(a[2], c[2])
     assert moe.moe_poll_status(ws) == 0
+
+
+def test_first_calls_may_be_captured():
+    """A process whose first calls are captured into a graph."""
+    code = """
+import torch
+from combine_softmax_top_b200 import moe, workloads as W
+s = W.spec("decode", T=40, E=64, k=4, H=128, I=128, compact=1)
+sh, g = moe.make_shape(s), moe.make_gate("sigmoid", 8, 4, 2)
+ws = torch.empty(moe.moe_workspace_bytes(sh), dtype=torch.uint8, device="cuda")
+moe.moe_workspace_init(sh, ws)
+l, b = torch.randn(40, 64, device="cuda"), torch.zeros(64, device="cuda")
+i, w = torch.empty(40, 4, dtype=torch.int32, device="cuda"), torch.empty(40, 4, device="cuda")
+x = torch.randn(40, 256, device="cuda")
+q, xs = torch.empty(40, 256, dtype=torch.int8, device="cuda"), torch.empty(40, device="cuda")
+wt, wsc = torch.ones(2048, 256, dtype=torch.int8, device="cuda"), torch.ones(2048, device="cuda")
+y, gl = torch.empty(40, 2048, device="cuda"), torch.empty_like(l)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    moe.moe_gate(sh, g, l, b, i, w, ws)
+    moe.moe_gate_backward(sh, g, l, i, w, gl)
+    moe.moe_quant_i8(x, q, xs)
+    moe.moe_gemm_i8(q, xs, wt, wsc, y, ws)
+graph.replay()
+torch.cuda.synchronize()
+assert moe.moe_poll_status(ws) == 0
+ref = (q.double().sum(1) * xs.double())[:, None].expand_as(y)
+assert torch.allclose(y.double(), ref, rtol=1e-6, atol=1e-6), (y, ref)
+assert abs(float(w.sum()) - 40) < 1e-3
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("compact", [0, 1])
