@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "ffn_common.cuh"
+#include "gemm_i8.cuh"
 
 namespace moe {
 namespace {
@@ -84,15 +85,6 @@ struct Params {
   int nk;        // K slabs
   int tiles;     // channel tiles of one expert
 };
-
-// g / (1 + exp(-g)) for results rounded to bf16: off by a few 2^-22 relative,
-// and by 1.6 |g| 2^-24 from the exponent (exactly g or 0 far out).
-__device__ __forceinline__ float quick_silu(float g) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return g * r;
-}
 
 // One unit: chunk `chunk` of expert e's rows, channel tile `tile`.
 struct Unit {
@@ -381,10 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
             if (kUp) b += sums[(r * owned + o) * 128 + 64 + n];
           }
           float f = (float)a * sw * xs[c];
-          if (kUp) f = (sizeof(O) == 2 ? quick_silu(f) : f / (1.f + expf(-f))) * ((float)b * su * xs[c]);
-          O* y = reinterpret_cast<O*>(p.y) + (j.row + c) * p.N + nn;
-          if constexpr (sizeof(O) == 2) *y = __float2bfloat16_rn(f);
-          else *y = f;
+          if (kUp) f = i8::swiglu<O>(f, (float)b * su * xs[c]);
+          i8::put(reinterpret_cast<O*>(p.y) + (j.row + c) * p.N + nn, f);
         }
       }
       __syncwarp();
@@ -434,10 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
           O* q = y + (int64_t)c * p.N;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (c + i < j.rows) {
-              if constexpr (sizeof(O) == 2) *q = __float2bfloat16_rn(f[i]);
-              else *q = f[i];
-            }
+            if (c + i < j.rows) i8::put(q, f[i]);
             q += p.N;
           }
         }
@@ -481,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
               for (int i = 0; i < 4; ++i) {
                 const int own = (int)(gate ? v[c + i] : v[16 + c + i]), far = other[(c + i) * 64 + ch];
                 const float g = (float)(gate ? own : far) * sw * s[i], u = (float)(gate ? far : own) * su * s[i];
-                f[c + i] = (sizeof(O) == 2 ? quick_silu(g) : g / (1.f + expf(-g))) * u;
+                f[c + i] = i8::swiglu<O>(g, u);
               }
             }
             store16(first, f);
@@ -581,6 +568,8 @@ cudaError_t launch_form(const GemmI8Args& a, int team) {
 }  // namespace
 
 cudaError_t launch_gemm_i8(const GemmI8Args& a) {
+  // a few dense rows that fit in shared memory
+  if (!a.win.offsets && a.d.M <= kFewRows && a.d.M * a.d.K <= 48 * 1024) return launch_gemm_i8_few(a);
   const int64_t fill = a.d.fill > 0 && a.d.fill < a.d.M ? a.d.fill : a.d.M, E = a.d.experts;
   const int64_t nk = ceil_div(a.d.K, kSlab), ch = a.wu ? 64 : 128;
   // units to expect: experts with rows, each of its share

@@ -1,0 +1,104 @@
+// int8 products of up to four dense rows (a decoded token), without tensor
+// cores: every weight is read once, and what counts is that all SMs read at
+// once and soon. A warp takes kCh channels and goes along K 512 bytes at a time,
+// 16 a lane: kCh loads of weights in flight for each step, the rows' pieces
+// from shared memory, four-way integer dot products, and one integer reduction
+// over the warp for every sum. Bound by latency and then by HBM.
+//
+// The tensor-core form needs 3.6 us for one slab of K (barriers, tensor memory,
+// tensor maps) and 0.24 us for each further one; here one row of 7168 x 2048
+// takes GEMV_A against 7.6 us, of 4096 x 7168 GEMV_B against 9.9 us.
+#include "gemm_i8.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kStep = 512;   // bytes of K a warp takes at a time
+
+__device__ __forceinline__ int dot16(int4 a, int4 b, int s) {
+  s = __dp4a(a.x, b.x, s);
+  s = __dp4a(a.y, b.y, s);
+  s = __dp4a(a.z, b.z, s);
+  return __dp4a(a.w, b.w, s);
+}
+
+template <int kM, int kCh, bool kUp, typename O>
+__global__ void __launch_bounds__(kThreads) gemm_i8_few_kernel(GemmI8Args a) {
+  extern __shared__ int4 sx[];   // [kM][K / 16]
+  const int lane = threadIdx.x & 31;
+  const int K16 = (int)(a.d.K / 16);
+  const int N = (int)a.d.N;
+  const int4* x = reinterpret_cast<const int4*>(a.x);
+  for (int i = threadIdx.x; i < kM * K16; i += kThreads) sx[i] = __ldg(x + i);
+  __syncthreads();
+  const int warps = gridDim.x * kWarps;
+  for (int64_t c0 = (int64_t)(blockIdx.x * kWarps + (threadIdx.x >> 5)) * kCh; c0 < N; c0 += (int64_t)warps * kCh) {
+    int acc[kM][kCh] = {}, up[kM][kUp ? kCh : 1] = {};
+#pragma unroll 4
+    for (int k = lane; k < K16; k += kStep / 16) {
+      int4 w[kCh], u[kUp ? kCh : 1];
+#pragma unroll
+      for (int c = 0; c < kCh; ++c) {
+        const int64_t at = (c0 + c < N ? c0 + c : c0) * K16 + k;   // channels past the last: the first once more
+        w[c] = __ldcs(reinterpret_cast<const int4*>(a.w) + at);
+        if (kUp) u[c] = __ldcs(reinterpret_cast<const int4*>(a.wu) + at);
+      }
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        const int4 xv = sx[m * K16 + k];
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) {
+          acc[m][c] = dot16(xv, w[c], acc[m][c]);
+          if (kUp) up[m][c] = dot16(xv, u[c], up[m][c]);
+        }
+      }
+    }
+    // lane m * kCh + c finishes row m, channel c
+    int mine = 0, mine_up = 0;
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int c = 0; c < kCh; ++c) {
+        const int s = __reduce_add_sync(0xffffffffu, acc[m][c]);
+        const int t = kUp ? __reduce_add_sync(0xffffffffu, up[m][c]) : 0;
+        if (lane == m * kCh + c) { mine = s; mine_up = t; }
+      }
+    const int m = lane / kCh;
+    const int64_t n = c0 + lane % kCh;
+    if (m < kM && n < N) {
+      const float xs = __ldg(a.xs + m);
+      float v = (float)mine * __ldg(a.ws + n) * xs;
+      if (kUp) v = i8::swiglu<O>(v, (float)mine_up * __ldg(a.wus + n) * xs);
+      i8::put(reinterpret_cast<O*>(a.y) + (int64_t)m * N + n, v);
+    }
+  }
+}
+
+template <int kM, int kCh, bool kUp>
+cudaError_t go(const GemmI8Args& a) {
+  const int64_t need = ceil_div(ceil_div(a.d.N, kCh), kWarps), most = 2 * (int64_t)a.num_sms;
+  const unsigned grid = (unsigned)(need < most ? need : most);
+  const size_t smem = (size_t)kM * (size_t)a.d.K;   // at most 48 KB (launch_gemm_i8)
+  if (a.d.out_dtype == MOE_F32) gemm_i8_few_kernel<kM, kCh, kUp, float><<<grid, kThreads, smem, a.stream>>>(a);
+  else gemm_i8_few_kernel<kM, kCh, kUp, __nv_bfloat16><<<grid, kThreads, smem, a.stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int kM>
+cudaError_t by_form(const GemmI8Args& a) {
+  // four channels a warp while that leaves every SM some (7168 channels: 12
+  // warps an SM), else one
+  const bool many = a.d.N >= 16 * (int64_t)a.num_sms;
+  if (a.wu) return many ? go<kM, 4, true>(a) : go<kM, 1, true>(a);
+  return many ? go<kM, 4, false>(a) : go<kM, 1, false>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_i8_few(const GemmI8Args& a) {
+  if (a.d.M == 1) return by_form<1>(a);
+  return a.d.M == 2 ? by_form<2>(a) : a.d.M == 3 ? by_form<3>(a) : by_form<4>(a);
+}
+
+}  // namespace moe

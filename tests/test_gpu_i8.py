@@ -188,7 +188,9 @@ def scales(n, seed, base):
                                    (17, 129, 4096), (64, 65, 272), (65, 1000, 528), (128, 128, 64), (129, 320, 2064),
                                    (300, 1001, 1552), (1000, 136, 96), (33, 2048, 7168), (257, 511, 400),
                                    (1, 100, 1040), (5, 40, 8192), (64, 130, 2064), (65, 300, 4112), (130, 64, 16384),
-                                   (2000, 4100, 160), (200, 4096, 1024)])
+                                   (2000, 4100, 160), (200, 4096, 1024),
+                                   (2, 5000, 528), (3, 2371, 1040), (4, 4099, 2064), (4, 70, 12288), (3, 16, 16400),
+                                   (5, 4099, 2064)])
 def test_dense_product(M, N, K, up, out, ws):
     x, w = ints((M, K), M), ints((N, K), N)
     xs, wsc = scales(M, 1, 1 / 64), scales(N, 2, 0.05 / K ** 0.5)
