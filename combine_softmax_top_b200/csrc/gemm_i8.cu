@@ -568,8 +568,16 @@ cudaError_t launch_form(const GemmI8Args& a, int team) {
 }  // namespace
 
 cudaError_t launch_gemm_i8(const GemmI8Args& a) {
-  // a few dense rows that fit in shared memory
-  if (!a.win.offsets && a.d.M <= kFewRows && a.d.M * a.d.K <= 48 * 1024) return launch_gemm_i8_few(a);
+  // A few dense rows without tensor cores: integer dot products keep up with the
+  // weights while rows x matrices are few, or the weights are soon read.
+  // Measured against the forms here, weights in L2: 7168 x 2048, one / four /
+  // eight rows 3.1 / 3.8 / 5.8 us against 7.5; 8192 x 8192 6.0 / 8.3 / 14.2
+  // against 14; with up 2048 x 7168 7.2 / 7.9 / 9.2 against 11, 4096 x 7168
+  // 10.4 / 17.8 / 25.9 against 14.7
+  const int64_t mats = a.wu ? 2 : 1, sums = a.d.M * mats, weights = mats * a.d.N * a.d.K;
+  if (!a.win.offsets && a.d.M <= kFewRows && a.d.M * a.d.K <= kFewBytes &&
+      (sums <= 4 || weights <= (sums <= 8 ? 32 : 16) * (int64_t)(1 << 20)))
+    return launch_gemm_i8_few(a);
   const int64_t fill = a.d.fill > 0 && a.d.fill < a.d.M ? a.d.fill : a.d.M, E = a.d.experts;
   const int64_t nk = ceil_div(a.d.K, kSlab), ch = a.wu ? 64 : 128;
   // units to expect: experts with rows, each of its share

@@ -26,8 +26,9 @@ __device__ __forceinline__ void put(__nv_bfloat16* y, float v) { *y = __float2bf
 
 }  // namespace i8
 
-// Dense products of up to kFewRows rows (gemm_i8_few.cu).
-constexpr int kFewRows = 4;
+// Dense products of up to kFewRows rows, of kFewBytes together (gemm_i8_few.cu).
+constexpr int kFewRows = 8;
+constexpr int64_t kFewBytes = 96 * 1024;
 cudaError_t launch_gemm_i8_few(const GemmI8Args& a);
 
 }  // namespace moe

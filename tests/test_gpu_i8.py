@@ -190,7 +190,8 @@ def scales(n, seed, base):
                                    (1, 100, 1040), (5, 40, 8192), (64, 130, 2064), (65, 300, 4112), (130, 64, 16384),
                                    (2000, 4100, 160), (200, 4096, 1024),
                                    (2, 5000, 528), (3, 2371, 1040), (4, 4099, 2064), (4, 70, 12288), (3, 16, 16400),
-                                   (5, 4099, 2064)])
+                                   (5, 4099, 2064), (8, 2400, 7168), (7, 300, 1040), (6, 2500, 16384), (1, 40, 98304),
+                                   (9, 2400, 1040)])
 def test_dense_product(M, N, K, up, out, ws):
     x, w = ints((M, K), M), ints((N, K), N)
     xs, wsc = scales(M, 1, 1 / 64), scales(N, 2, 0.05 / K ** 0.5)
