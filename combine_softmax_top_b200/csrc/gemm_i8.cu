@@ -12,8 +12,8 @@
 // memory: the main loop is the same as without.
 //
 // Per CTA (320 threads): warp 0 streams K slabs of 128 bytes into a ring of
-// stages with TMA, warp 1 issues the MMAs into one of two accumulators, warps
-// 2-9 read the other one back, scale and store. Three forms:
+// stages with TMA, warp 1 issues the MMAs into tensor memory, warps
+// 2-9 read finished ones back, scale and store. Three forms:
 //   kOne    chunks of 64 rows, one CTA: a decode batch reads every weight once,
 //           and the many small stages keep the loads in flight that HBM needs
 //   kSplit  the same with a unit's K slabs split over the CTAs of a cluster,
@@ -21,9 +21,12 @@
 //           sums of a row into the shared memory of the CTA that owns the row
 //           (row mod cluster size), which adds and stores them (integers: the
 //           order changes nothing)
-//   kPair   chunks of 256 rows, a CTA pair (M = 256 over two SMs, each holding
-//           half of the rows): for many rows an expert, where the tensor cores
-//           and the L2's delivery of operands bound it
+//   kPair   chunks of 256 rows, or up to 288 where that saves one, a CTA pair
+//           (M = 256 over two SMs, each holding half of the rows): for many rows
+//           an expert, where the tensor cores and the L2's delivery of operands
+//           bound it. The 512 columns of tensor memory are a ring: a unit takes
+//           as many as it has rows, and the next one starts when enough of the
+//           last but one's are read, 32 at a time.
 // Every wait is bounded: on expiry the kernel latches MOE_ERR_TIMEOUT, drains
 // its copies and MMAs, frees tensor memory and exits.
 #include <algorithm>
@@ -52,13 +55,14 @@ enum : int { kOne, kSplit, kPair };
 template <int kForm, bool kUp>
 struct Form {
   static constexpr int kG = kForm == kPair ? 2 : 1;           // CTAs of one MMA
-  static constexpr int kRows = kG == 2 ? 256 : 64;            // rows of a chunk: MMA columns
+  static constexpr int kFull = kG == 2 ? 256 : 64;            // rows of a chunk: MMA columns
+  static constexpr int kRows = kG == 2 ? 288 : 64;            // and of the largest
   static constexpr int kBRows = kRows / kG;                   // of them in this CTA's shared memory
   static constexpr int kCh = kUp ? 64 : 128;                  // channels a CTA
   static constexpr int kStage = kABytes + kBRows * kSlab;
   // kSplit: [CTA][rows owned][128 A rows] int32, the sums of this CTA's rows; else with up
-  // [set][gate, up][16 rows][64 channels] int32
-  static constexpr int kXchg = kForm == kSplit ? kRows * 128 * 4 : kUp ? 2 * 2 * 16 * 64 * 4 : 0;
+  // [set][gate, up][8 rows][64 channels] int32
+  static constexpr int kXchg = kForm == kSplit ? kRows * 128 * 4 : kUp ? 2 * 2 * 8 * 64 * 4 : 0;
   static constexpr int kXs = 2 * kRows * 4;                   // row scales, two units
   static constexpr int kTab = (kMaxExperts + 1) * 4 + 12;
   static constexpr int kCtl = 512;
@@ -68,8 +72,10 @@ struct Form {
   static constexpr int kOffTab = kOffXs + kXs;
   static constexpr int kOffCtl = (kOffTab + kTab + 15) / 16 * 16;
   static constexpr int kSmem = kOffCtl + kCtl + 1024;         // and alignment slack
-  static constexpr uint32_t kTmemCols = 2 * kRows;
-  static_assert(kSmem <= kMaxDynSmem && (2 * kStages + 7) * 8 <= kCtl - 32, "shared memory");
+  static constexpr uint32_t kTmemCols = 2 * kFull;            // kPair: the ring; else two accumulators
+  static constexpr int kGran = 32;                            // columns given back at a time
+  static_assert(kSmem <= kMaxDynSmem && (2 * kStages + 7 + (int)kTmemCols / kGran) * 8 <= kCtl - 32, "shared memory");
+  static_assert(kForm != kPair || kStages >= 6, "stages of a pair");
 };
 
 struct Params {
@@ -84,6 +90,7 @@ struct Params {
   int64_t M, N;
   int nk;        // K slabs
   int tiles;     // channel tiles of one expert
+  int wide;      // kPair: chunks of more than kFull rows may be taken
 };
 
 // One unit: chunk `chunk` of expert e's rows, channel tile `tile`.
@@ -106,6 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
   uint64_t* drain = acc_empty + 2;
   uint64_t* part_full = drain + 1;                        // kSplit: all CTAs' sums of this one's rows are here
   uint64_t* part_free = part_full + 1;                    // kSplit: all CTAs have read what they got
+  uint64_t* col_free = part_free + 1;                     // kPair, CTA 0: [16] both CTAs have read these 32 columns
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + F::kCtl - 32);
   volatile int* epi_ok = abort_flag + 1;                  // [2]
   volatile int* part_ok = epi_ok + 2;
@@ -133,6 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     ptx::mbar_init(drain, 1);
     ptx::mbar_init(part_full, 8 * parts);
     ptx::mbar_init(part_free, 8 * parts);
+    if constexpr (kForm == kPair)
+      for (int g = 0; g < (int)F::kTmemCols / F::kGran; ++g) ptx::mbar_init(col_free + g, 8);   // a set's warps, two CTAs
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -145,9 +155,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
       ptx::tmem_relinquish();
     }
   }
+  // MMA columns for that many rows
+  auto columns = [](int rows) { return (rows + 16 * kG - 1) / (16 * kG) * (16 * kG); };
+  // Chunks of a window. A unit's time goes like its columns + 72 (measured, per
+  // channel tile of K = 7168: 160 columns 20 us, 256 29 us), so that chunks of
+  // more than kFull rows are taken where that saves 3 %: 270 rows are one chunk
+  // of 288 columns, not 160 and 128.
+  auto chunks = [&](int rows) {
+    const int c = (rows + F::kFull - 1) / F::kFull, d = (rows + F::kRows - 1) / F::kRows;
+    if (kForm != kPair || !p.wide || d >= c) return c;
+    auto cost = [&](int n) { return (int64_t)n * (72 + columns((rows + n - 1) / n)); };
+    return cost(d) * 33 < cost(c) * 32 ? d : c;
+  };
   if (warp == 2)   // first chunk of every expert
-    window_prefix(p.win, p.M, (p.M + F::kRows - 1) / F::kRows + E, [](int n) { return (n + F::kRows - 1) / F::kRows; },
-                  tab);
+    window_prefix(p.win, p.M, (p.M + F::kFull - 1) / F::kFull + E, chunks, tab);
   ptx::tc_fence_before();
   if constexpr (kForm != kOne) ptx::cluster_sync();   // every CTA's barriers and tensor memory exist
   else __syncthreads();
@@ -157,8 +178,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
 
   auto remote = [&](const void* q, uint32_t r) { return ptx::mapa_shared(ptx::smem_u32(q), r); };
 
-  // MMA columns for that many rows
-  auto columns = [](int rows) { return (rows + 16 * kG - 1) / (16 * kG) * (16 * kG); };
   // Unit u. Within an expert: bands of kBand chunks, in a band channel tile by
   // channel tile, so that the workers of one moment share few rows and few
   // channels in L2.
@@ -181,13 +200,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     const int chunk = (int)(band * kBand + w - (uint32_t)r.tile * bh);
     int64_t row0;
     // an expert's chunks are of one size, so that the units that follow one
-    // another cost alike (256 + 14 rows: 160 + 110)
+    // another cost alike
     const int rows = window_rows(p.win, lo, p.M, &row0);
     const int each = columns((int)(((uint32_t)rows + (uint32_t)nc - 1u) / (uint32_t)nc));
     const int left_rows = rows - chunk * each;
     r.rows = left_rows < each ? left_rows : each;
     r.row = row0 + (int64_t)chunk * each;
     return r;
+  };
+  // kPair: of n columns from `at` on, those of the first MMA: up to the ring's
+  // end, and 256 at most. A second one takes the rest (288 or fewer are left
+  // with 256 or fewer).
+  auto first_columns = [](int at, int n) {
+    if (kForm != kPair) return n;
+    const int to_end = (int)F::kTmemCols - at;
+    return n < to_end ? (n < 256 ? n : 256) : (to_end < 256 ? to_end : 256);
   };
 
   if (warp == 0) {
@@ -201,11 +228,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     uint32_t armed = 0, armed_parity = 0;
     const uint64_t pol = ptx::policy_evict_first();   // kOne, kSplit: weights are read once
     bool ok = true;
+    int at = 0;   // kPair: the unit's first column
     for (int u = worker; ok && u < units; u += workers) {
       const Unit j = unit(u);
-      const int n = columns(j.rows) / kG;                       // rows this CTA loads
+      const int cols = columns(j.rows), c1 = first_columns(at, cols);
+      at = (at + cols) % (int)F::kTmemCols;
+      const int n = cols / kG;                                  // rows this CTA loads
+      const int n1 = c1 / kG, n2 = n - n1;                      // its halves of the two MMAs' columns
       const int wrow = (int)(j.e * p.N + (int64_t)j.tile * (kG * F::kCh) + rank * F::kCh);
-      const int xrow = (int)(j.row + rank * n);
+      const int xrow = (int)(j.row + rank * n1), xrow2 = (int)(j.row + c1 + rank * n2);
       for (int k = k_first; k < k_end; ++k) {
         int good = 1;
         if (lane == 0) good = wait_bar(empty + stage, phase ^ 1u, abort_flag, p.hdr, 0x48000000u | stage);
@@ -217,23 +248,29 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
           const int kx = k * kSlab;
           uint8_t* sx = st + kABytes;
           // rows in the fewest boxes, each map at a fixed parameter address
-          auto rows = [&](auto load) {
+          auto rows = [&](int m, int to, int from, auto load) {
             int r = 0;
-            if (F::kBRows >= 128 && n & 128) { load(&p.tm_x[3], r); r += 128; }
-            if (n & 64) { load(&p.tm_x[2], r); r += 64; }
-            if (n & 32) { load(&p.tm_x[1], r); r += 32; }
-            if (n & 16) load(&p.tm_x[0], r);
+            if (F::kBRows >= 128 && m & 128) { load(&p.tm_x[3], to, from); r = 128; }
+            if (m & 64) { load(&p.tm_x[2], to + r, from + r); r += 64; }
+            if (m & 32) { load(&p.tm_x[1], to + r, from + r); r += 32; }
+            if (m & 16) load(&p.tm_x[0], to + r, from + r);
           };
           if constexpr (kG == 2) {
             const uint32_t fb = remote(full + stage, 0);
             ptx::tma_load_2d_pair(st, &p.tm_w, fb, kx, wrow);
             if (kUp) ptx::tma_load_2d_pair(st + 64 * kSlab, &p.tm_wu, fb, kx, wrow);
-            rows([&](const CUtensorMap* m, int r) { ptx::tma_load_2d_pair(sx + r * kSlab, m, fb, kx, xrow + r); });
+            auto load = [&](const CUtensorMap* m, int to, int from) {
+              ptx::tma_load_2d_pair(sx + to * kSlab, m, fb, kx, from);
+            };
+            rows(n1, 0, xrow, load);
+            if (n2) rows(n2, n1, xrow2, load);
           } else {
             uint64_t* fb = full + stage;
             ptx::tma_load_2d_hint(st, &p.tm_w, fb, kx, wrow, pol);
             if (kUp) ptx::tma_load_2d_hint(st + 64 * kSlab, &p.tm_wu, fb, kx, wrow, pol);
-            rows([&](const CUtensorMap* m, int r) { ptx::tma_load_2d(sx + r * kSlab, m, fb, kx, xrow + r); });
+            rows(n, 0, xrow, [&](const CUtensorMap* m, int to, int from) {
+              ptx::tma_load_2d(sx + to * kSlab, m, fb, kx, from);
+            });
           }
         }
         __syncwarp();
@@ -256,15 +293,29 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     // ---------------------------------------------------------------- MMA issuer (CTA 0)
     if (rank == 0) {
       uint32_t stage = 0, phase = 0, i = 0;
+      uint32_t uses = 0;   // kPair: bit g: parity of the uses of columns 32 g ..
+      int at = 0;
       bool ok = true;
       for (int u = worker; ok && u < units; u += workers, ++i) {
         const uint32_t slot = i & 1u, use = (i >> 1) & 1u;
+        const int cols = columns(unit(u).rows), c1 = first_columns(at, cols);
         int good = 1;
-        if (lane == 0) good = wait_bar<kG == 2>(acc_empty + slot, use ^ 1u, abort_flag, p.hdr, 0x58000000u | slot);
-        if (!__shfl_sync(0xffffffffu, good, 0)) break;
+        if (lane == 0) good = wait_bar(acc_empty + slot, use ^ 1u, abort_flag, p.hdr, 0x58000000u | slot);
+        if constexpr (kForm == kPair) {   // and the unit's columns are free, lane by lane
+          constexpr int kGrans = (int)F::kTmemCols / F::kGran;
+          const int g = (at / F::kGran + lane) % kGrans;
+          const bool mine = lane < cols / F::kGran;
+          if (mine && good) good = wait_bar(col_free + g, ((uses >> g) & 1u) ^ 1u, abort_flag, p.hdr, 0x59000000u);
+          uses ^= __reduce_or_sync(0xffffffffu, mine ? 1u << g : 0u);
+        }
+        if (!__all_sync(0xffffffffu, good)) break;
         ptx::tc_fence_after();
-        const uint32_t d = tmem + slot * F::kRows;
-        const uint32_t idesc = ptx::idesc_i8(128 * kG, columns(unit(u).rows));
+        const uint32_t d = tmem + (kForm == kPair ? (uint32_t)at : slot * F::kRows);
+        const uint32_t d2 = tmem + (uint32_t)((at + c1) % (int)F::kTmemCols);   // kPair: of the second MMA
+        const uint32_t idesc = ptx::idesc_i8(128 * kG, c1), idesc2 = ptx::idesc_i8(128 * kG, cols - c1);
+        const uint64_t b2_off = (uint64_t)(c1 / kG * kSlab) >> 4;
+        const bool two = c1 < cols;
+        at = (at + cols) % (int)F::kTmemCols;
         for (int k = k_first; k < k_end; ++k) {
           if (lane == 0) good = wait_bar(full + stage, phase, abort_flag, p.hdr, 0x68000000u | stage);
           if (!__shfl_sync(0xffffffffu, good, 0)) { ok = false; break; }
@@ -276,6 +327,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
             for (int kk = 0; kk < 4; ++kk) {   // 32 bytes of K per MMA
               if constexpr (kG == 2) ptx::mma_i8_pair(d, a + 2 * kk, b + 2 * kk, idesc, k > k_first || kk ? 1u : 0u);
               else ptx::mma_i8(d, a + 2 * kk, b + 2 * kk, idesc, k > k_first || kk ? 1u : 0u);
+            }
+            if (kForm == kPair && two) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                ptx::mma_i8_pair(d2, a + 2 * kk, b + b2_off + 2 * kk, idesc2, k > k_first || kk ? 1u : 0u);
             }
             if constexpr (kG == 2) {
               ptx::mma_commit_pair(remote(empty + stage, 0));
@@ -314,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     const int q = warp & 3, et = threadIdx.x - 64, set = et >> 7;
     const int arow = q * 32 + lane;
     const int ch = kUp ? arow & 63 : arow;           // channel of the CTA's tile
-    int* xg = reinterpret_cast<int*>(smem + F::kOffXchg) + set * 2 * 16 * 64;   // [16][64]
-    int* xu = xg + 16 * 64;
+    int* xg = reinterpret_cast<int*>(smem + F::kOffXchg) + set * 2 * 8 * 64;   // [8][64]
+    int* xu = xg + 8 * 64;
     float* xs_all = reinterpret_cast<float*>(smem + F::kOffXs);
     // kSplit: this CTA's sums to the owners of their rows, then its own rows
     auto split_epilogue = [&](const Unit& j, uint32_t slot, uint32_t use, uint32_t turn) -> bool {
@@ -383,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
       return true;
     };
     uint32_t i = 0;
+    int at = 0;   // kPair: the unit's first column
     for (int u = worker; u < units; u += workers, ++i) {
       const Unit j = unit(u);
       const uint32_t slot = i & 1u, use = (i >> 1) & 1u;
@@ -395,14 +452,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
       const bool real = n0 < p.N;
       const float sw = real ? __ldg(p.ws + j.e * p.N + n0) : 0.f;
       const float su = kUp && real ? __ldg(p.wus + j.e * p.N + n0) : 0.f;
-      if (et < j.rows) xs[et] = __ldg(p.xs + j.row + et);
+      for (int r = et; r < j.rows; r += kEpiThreads) xs[r] = __ldg(p.xs + j.row + r);
       // one thread waits and tells the others, so that all leave together
       if (et == 0) epi_ok[slot] = wait_bar(acc_full + slot, use, abort_flag, p.hdr, 0x78000000u | slot);
       ptx::named_barrier(1, kEpiThreads);
       if (!epi_ok[slot]) break;
       while (!ptx::mbar_try_wait(acc_full + slot, use)) {}   // completed: returns at once
       ptx::tc_fence_after();
-      const uint32_t d = tmem + slot * F::kRows + ((uint32_t)(q * 32) << 16);
+      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+      const int d = kForm == kPair ? at : (int)slot * F::kRows;
+      at = (at + columns(j.rows)) % (int)F::kTmemCols;
       const int64_t tile0 = n0 - ch;   // the CTA's first channel
       // bf16: two lanes exchange half of their rows, so that each stores two
       // neighbouring channels at once
@@ -431,8 +490,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
       };
       for (int c0 = 32 * set; c0 < j.rows; c0 += 64) {
         uint32_t v[32];
-        ptx::tmem_ld_x32(d + c0, v);
+        const int col = kForm == kPair ? (d + c0) % (int)F::kTmemCols : d + c0;
+        ptx::tmem_ld_x32(lanes + (uint32_t)col, v);
         ptx::tmem_wait_ld();
+        if constexpr (kForm == kPair) {   // the columns are in registers: give them back
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (rank == 0) ptx::mbar_arrive(col_free + col / F::kGran);
+            else ptx::mbar_arrive_remote(remote(col_free + col / F::kGran, 0));
+          }
+        }
         float f[16];
         if constexpr (!kUp) {
 #pragma unroll
@@ -449,31 +517,35 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
             store16(c0 + h, f);
           }
         } else {
-          // gate warps finish the batch's first 16 columns, up warps the last
+          // gate warps finish the batch's first 16 columns, up warps the last; eight
+          // at a time change hands
           const bool gate = q < 2;
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (gate) xg[c * 64 + ch] = (int)v[16 + c];
-            else xu[c * 64 + ch] = (int)v[c];
-          }
-          ptx::named_barrier(2 + set, 128);
           const int first = c0 + (gate ? 0 : 16);
-          if (first < j.rows) {
-            const int* other = gate ? xu : xg;
 #pragma unroll
-            for (int c = 0; c < 16; c += 4) {
-              const float4 s4 = *reinterpret_cast<const float4*>(xs + first + c);
-              const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+          for (int h = 0; h < 16; h += 8) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int own = (int)(gate ? v[c + i] : v[16 + c + i]), far = other[(c + i) * 64 + ch];
-                const float g = (float)(gate ? own : far) * sw * s[i], u = (float)(gate ? far : own) * su * s[i];
-                f[c + i] = i8::swiglu<O>(g, u);
+            for (int c = 0; c < 8; ++c) {
+              if (gate) xg[c * 64 + ch] = (int)v[16 + h + c];
+              else xu[c * 64 + ch] = (int)v[h + c];
+            }
+            ptx::named_barrier(2 + set, 128);
+            if (first + h < j.rows) {
+              const int* other = gate ? xu : xg;
+#pragma unroll
+              for (int c = 0; c < 8; c += 4) {
+                const float4 s4 = *reinterpret_cast<const float4*>(xs + first + h + c);
+                const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int own = (int)(gate ? v[h + c + i] : v[16 + h + c + i]), far = other[(c + i) * 64 + ch];
+                  const float g = (float)(gate ? own : far) * sw * s[i], u = (float)(gate ? far : own) * su * s[i];
+                  f[h + c + i] = i8::swiglu<O>(g, u);
+                }
               }
             }
-            store16(first, f);
+            ptx::named_barrier(2 + set, 128);
           }
-          ptx::named_barrier(2 + set, 128);
+          if (first < j.rows) store16(first, f);
         }
       }
       ptx::tc_fence_before();
@@ -499,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
 
 // team: CTAs of a worker (the cluster), 1, 2 or 4
 template <int kForm, bool kUp, typename O>
-cudaError_t launch(const GemmI8Args& a, int team) {
+cudaError_t launch(const GemmI8Args& a, int team, bool wide) {
   using F = Form<kForm, kUp>;
   constexpr int kMaxDevices = 64;
   static std::atomic<int> resident[kMaxDevices][3];   // clusters of 1, 2, 4 at once on each device, 0 = not asked yet
@@ -526,6 +598,7 @@ cudaError_t launch(const GemmI8Args& a, int team) {
   p.N = N;
   p.nk = (int)ceil_div(K, kSlab);
   p.tiles = (int)ceil_div(N, F::kG * F::kCh);
+  p.wide = wide ? 1 : 0;
 
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
@@ -553,16 +626,16 @@ cudaError_t launch(const GemmI8Args& a, int team) {
     known.store(workers, std::memory_order_release);
   }
   // no more workers than the most units there can be
-  const int64_t most = (ceil_div(a.d.M, F::kRows) + (a.win.offsets ? E : 0)) * p.tiles;
+  const int64_t most = (ceil_div(a.d.M, F::kFull) + (a.win.offsets ? E : 0)) * p.tiles;
   cfg.gridDim.x = (unsigned)(team * std::min<int64_t>(std::min(workers, fit), most));
   return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<kForm, kUp, O>, p);
 }
 
 template <int kForm>
-cudaError_t launch_form(const GemmI8Args& a, int team) {
+cudaError_t launch_form(const GemmI8Args& a, int team, bool wide = false) {
   const bool f32 = a.d.out_dtype == MOE_F32;
-  if (a.wu) return f32 ? launch<kForm, true, float>(a, team) : launch<kForm, true, __nv_bfloat16>(a, team);
-  return f32 ? launch<kForm, false, float>(a, team) : launch<kForm, false, __nv_bfloat16>(a, team);
+  if (a.wu) return f32 ? launch<kForm, true, float>(a, team, wide) : launch<kForm, true, __nv_bfloat16>(a, team, wide);
+  return f32 ? launch<kForm, false, float>(a, team, wide) : launch<kForm, false, __nv_bfloat16>(a, team, wide);
 }
 
 }  // namespace
@@ -588,7 +661,7 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a) {
   // rounds of units. Measured, pairs / single CTAs: 200 x 4096 x 7168 28 / 18 us;
   // 32 experts of gate/up 2048 x 7168, 64 rows each 180 / 164 us, 128 rows 186 / 234
   if (a.num_sms >= 2 && 3 * ceil_div(pairs, a.num_sms / 2) <= 2 * ceil_div(ones, a.num_sms))
-    return launch_form<kPair>(a, 2);
+    return launch_form<kPair>(a, 2, pairs >= a.num_sms);   // wide chunks where two rounds are full anyway
   // A CTA takes 0.24 us a slab; sharing K over 2 or 4 costs 2 to 4 us. Measured,
   // 1 / 2 / 4 CTAs: one row, 4096 x 7168 17.2 / 12.3 / 9.9 us, 64 rows 18.0 /
   // 15.1 / 12.0; 7168 x 2048 7.6 / 7.6 us, 64 rows 8.2 / 10.2
