@@ -25,6 +25,28 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kMaxExperts = 1024;
 
+// Two binary32 numbers an instruction, each rounded to nearest as one alone.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // 16 bytes of consecutive elements, as loaded.
 template <typename T>
 struct Piece {
@@ -39,27 +61,33 @@ struct Piece {
     if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
     else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
   }
-  // |x| as bits: ordered like the values, NaN and infinity above all numbers
+  // |x| as bits, ordered like the values, NaN and infinity above all numbers:
+  // of fp32 as they are, of bf16 two elements side by side (most_of joins them)
   __device__ __forceinline__ uint32_t most(uint32_t m) const {
-    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFF0000u, (w[i] << 16) & 0x7FFF0000u));
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) m = max(m, w[i] & 0x7FFFFFFFu);
+      else m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
     }
     return m;
   }
+  static __device__ __forceinline__ uint32_t most_of(uint32_t m) {
+    if constexpr (sizeof(T) == 4) return m;
+    else return max(m & 0xFFFF0000u, m << 16);
+  }
   template <bool kTiny>
   __device__ __forceinline__ void quantise(float s, float y, int8_t* q) const {
+    const uint64_t y2 = two(y, y), minus_s = two(-s, -s), magic = two(12582912.f, 12582912.f);   // 1.5 * 2^23
     float t[kN];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const float x = kTiny ? at(i) * 0x1p64f : at(i);
-      float v = __fmul_rn(x, y);
-      v = __fmaf_rn(__fmaf_rn(-v, s, x), y, v);
-      v = __fmaf_rn(__fmaf_rn(-v, s, x), y, v);
-      t[i] = __fadd_rn(v, 12582912.f);   // 1.5 * 2^23
+    for (int i = 0; i < kN; i += 2) {   // two elements an instruction
+      uint64_t x = two(at(i), at(i + 1));
+      if (kTiny) x = mul2(x, two(0x1p64f, 0x1p64f));
+      uint64_t v = mul2(x, y2);
+      v = fma2(fma2(v, minus_s, x), y2, v);
+      v = fma2(fma2(v, minus_s, x), y2, v);
+      v = add2(v, magic);
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(t[i]), "=f"(t[i + 1]) : "l"(v));
     }
     uint32_t b[kN / 4];
 #pragma unroll
@@ -123,6 +151,7 @@ quant_i8_kernel(const T* __restrict__ x, int64_t rows, int cols, RowWindows win,
       more.load(xr + c);
       m = more.most(m);
     }
+    m = Piece<T>::most_of(m);
     if constexpr (kTeam >= 32) {
       m = __reduce_max_sync(0xffffffffu, m);
     } else {
