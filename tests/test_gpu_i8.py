@@ -267,6 +267,33 @@ def test_grouped_product(g, up, out, fill, ws):
     assert bool((y[~filled.cuda()] == 77.0).all())
 
 
+@pytest.mark.parametrize("up", [False, True])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_a_row_has_the_same_bits_in_any_company(up, out, ws):
+    """Alone, among few or many rows, dense or in a window: whichever kernel and
+    tiles that takes, the sums are exact and the arithmetic after them the same."""
+    M, N, K = 1200, 3000, 3200
+    x, xs = ints((M, K), 1).cuda(), scales(M, 2, 1 / 64).cuda()
+    w, wsc = ints((N, K), 3).cuda(), scales(N, 4, 0.05 / K ** 0.5).cuda()
+    wu, us = (ints((N, K), 5).cuda(), scales(N, 6, 0.05 / K ** 0.5).cuda()) if up else (None, None)
+    full = torch.empty(M, N, dtype=DT[out], device="cuda")
+    moe.moe_gemm_i8(x, xs, w, wsc, full, ws, w_up=wu, up_scale=us)
+    for m in (1, 2, 4, 8, 9, 33, 64, 65, 200, 300, 700):
+        a = (7 * m) % (M - m)
+        y = torch.empty(m, N, dtype=DT[out], device="cuda")
+        moe.moe_gemm_i8(x[a:a + m].clone(), xs[a:a + m].clone(), w, wsc, y, ws, w_up=wu, up_scale=us)
+        assert torch.equal(y, full[a:a + m]), m
+    three = dict(w_up=None if wu is None else wu.view(3, 1000, K), up_scale=None if us is None else us.view(3, 1000))
+    off = torch.tensor([3, 700, 1000], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor([290, 1, 150], dtype=torch.int32, device="cuda")
+    for fill in (0, 3, 441):
+        y = torch.empty(M, 1000, dtype=DT[out], device="cuda")
+        moe.moe_gemm_i8(x, xs, w.view(3, 1000, K), wsc.view(3, 1000), y, ws, offsets=off, counts=cnt, fill=fill, **three)
+        for e, (o, c) in enumerate(zip(off.tolist(), cnt.tolist())):
+            assert torch.equal(y[o:o + c], full[o:o + c, 1000 * e:1000 * (e + 1)]), (fill, e)
+    assert moe.moe_poll_status(ws) == 0
+
+
 def test_windows_out_of_range_are_cut(ws):
     M, N, K = 200, 64, 128
     x, xs, w = ints((M, K), 1), scales(M, 2, 1.0), ints((5, N, K), 3)
@@ -357,6 +384,12 @@ def test_streams_graphs_and_two_calls_at_once(ws):
             linear(x, *b)
         linear(x, *a)
     torch.cuda.synchronize()
+    assert torch.equal(a[2], b[2])
+    b[2].zero_()                                            # a stream given by argument
+    st.wait_stream(torch.cuda.current_stream())
+    moe.moe_quant_i8(x, b[0], b[1], stream=st)
+    moe.moe_gemm_i8(b[0], b[1], w, wsc, b[2], ws, stream=st)
+    st.synchronize()
     assert torch.equal(a[2], b[2])
     sx, c = x.clone(), bufs()
     graph = torch.cuda.CUDAGraph()
