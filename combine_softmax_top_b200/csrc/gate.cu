@@ -670,11 +670,12 @@ cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits
     // a lane for every slot and, where the keys are not exact, the best one left
     const int lanes = std::max(k + (sizeof(L) == 2 && !bias ? 0 : 1), (int)g.groups);
     // Fewer lanes a token once the SMs are full of warps anyway. Measured, warp
-    // against part: 16384 x 128 bf16 9.6 / 8.2 us, 4096 x 128 3.8 / 4.5;
-    // 65536 x 256 f32 with bias and groups 71 / 62, 4096 x 256 8.2 / 9.2
-    if (T >= 8192 && lanes <= 8 && E <= 128)
+    // against part: 4096 x 128 bf16 3.7 / 3.4 us, 2048 the same, 512 2.5 / 3.0;
+    // 8192 x 64 f32 6.5 / 5.5, 4096 4.6 / 4.6; 16384 x 256 f32 with bias and groups
+    // 17.2 / 16.4, 8192 10.6 / 11.0
+    if (T >= 4096 && lanes <= 8 && E <= 128)
       return E <= 64 ? go(gate_kernel<L, kSig, 8, 8>, l, 8) : go(gate_kernel<L, kSig, 16, 8>, l, 8);
-    if (T >= 32768 && lanes <= 16 && E <= 256)
+    if (T >= (E <= 128 ? 8192 : 12288) && lanes <= 16 && E <= 256)
       return E <= 128 ? go(gate_kernel<L, kSig, 8, 16>, l, 16) : go(gate_kernel<L, kSig, 16, 16>, l, 16);
     if (E <= 128) return go(gate_kernel<L, kSig, 4, 32>, l, 32);
     if (E <= 256) return go(gate_kernel<L, kSig, 8, 32>, l, 32);

@@ -302,7 +302,7 @@ def _begin(fn: str, name: str, t, stream):
     """(current device, stream handle) of a call whose first tensor is t."""
     if not t.is_cuda:
         raise ValueError(f"{fn}: {name} must be on the current CUDA device, is on {t.device}")
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()   # current_device(), whose check of an initialised CUDA t has passed
     return dev, (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
