@@ -13,7 +13,7 @@
 //
 // Per CTA (320 threads): warp 0 streams K slabs of 128 bytes into a ring of
 // stages with TMA, warp 1 issues the MMAs into tensor memory, warps
-// 2-9 read finished ones back, scale and store. Three forms:
+// 2-9 read finished ones back, scale and store. Four forms:
 //   kOne    chunks of 64 rows, one CTA: a decode batch reads every weight once,
 //           and the many small stages keep the loads in flight that HBM needs
 //   kSplit  the same with a unit's K slabs split over the CTAs of a cluster,
@@ -27,6 +27,8 @@
 //           bound it. The 512 columns of tensor memory are a ring: a unit takes
 //           as many as it has rows, and the next one starts when enough of the
 //           last but one's are read, 32 at a time.
+//   kPair128  the same with chunks of up to 128 rows, whose eight smaller stages
+//           keep more loads in flight
 // Measured from a cold start: 8192 x 4096 x 7168 141 us, 3.4 POP/s (kPair, 87 % of
 // the tensor pipe; 173 us at the power cap); gate/up of 32 experts, 2 x 2048 x
 // 7168, with 128 rows 148 us = 6.3 TB/s (kOne), with 8192 rows 205 us (kPair, 5.1
@@ -35,6 +37,7 @@
 // its copies and MMAs, frees tensor memory and exits.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <type_traits>
 
@@ -54,13 +57,14 @@ constexpr int kEpiThreads = 256;
 constexpr int kMaxExperts = 1024;
 constexpr int kBand = 8;           // chunks that share each channel tile in turn (unit order)
 
-enum : int { kOne, kSplit, kPair };
+enum : int { kOne, kSplit, kPair, kPair128 };
 
 template <int kForm, bool kUp>
 struct Form {
-  static constexpr int kG = kForm == kPair ? 2 : 1;           // CTAs of one MMA
-  static constexpr int kFull = kG == 2 ? 256 : 64;            // rows of a chunk: MMA columns
-  static constexpr int kRows = kG == 2 ? 288 : 64;            // and of the largest
+  static constexpr bool kPaired = kForm >= kPair;
+  static constexpr int kG = kPaired ? 2 : 1;                  // CTAs of one MMA
+  static constexpr int kFull = kForm == kPair ? 256 : kPaired ? 128 : 64;   // rows of a chunk: MMA columns
+  static constexpr int kRows = kForm == kPair ? 288 : kFull;  // and of the largest
   static constexpr int kBRows = kRows / kG;                   // of them in this CTA's shared memory
   static constexpr int kCh = kUp ? 64 : 128;                  // channels a CTA
   static constexpr int kStage = kABytes + kBRows * kSlab;
@@ -76,10 +80,10 @@ struct Form {
   static constexpr int kOffTab = kOffXs + kXs;
   static constexpr int kOffCtl = (kOffTab + kTab + 15) / 16 * 16;
   static constexpr int kSmem = kOffCtl + kCtl + 1024;         // and alignment slack
-  static constexpr uint32_t kTmemCols = 2 * kFull;            // kPair: the ring; else two accumulators
+  static constexpr uint32_t kTmemCols = 2 * kFull;            // pairs: the ring; else two accumulators
   static constexpr int kGran = 32;                            // columns given back at a time
   static_assert(kSmem <= kMaxDynSmem && (2 * kStages + 7 + (int)kTmemCols / kGran) * 8 <= kCtl - 32, "shared memory");
-  static_assert(kForm != kPair || kStages >= 6, "stages of a pair");
+  static_assert(!kPaired || kStages >= 6, "stages of a pair");
 };
 
 struct Params {
@@ -117,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
   uint64_t* drain = acc_empty + 2;
   uint64_t* part_full = drain + 1;                        // kSplit: all CTAs' sums of this one's rows are here
   uint64_t* part_free = part_full + 1;                    // kSplit: all CTAs have read what they got
-  uint64_t* col_free = part_free + 1;                     // kPair, CTA 0: [16] both CTAs have read these 32 columns
+  uint64_t* col_free = part_free + 1;                     // pairs, CTA 0: both CTAs have read these 32 columns
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + F::kCtl - 32);
   volatile int* epi_ok = abort_flag + 1;                  // [2]
   volatile int* part_ok = epi_ok + 2;
@@ -125,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
   int* tab = reinterpret_cast<int*>(smem + F::kOffTab);   // [experts + 1] first chunk of each expert
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = kForm == kPair ? ptx::cluster_ctarank() : 0u;   // CTA of the MMA
+  const uint32_t rank = F::kPaired ? ptx::cluster_ctarank() : 0u;   // CTA of the MMA
   const uint32_t part = kForm == kSplit ? ptx::cluster_ctarank() : 0u;  // share of K
   const uint32_t parts = kForm == kSplit ? ptx::cluster_nctarank() : 1u;
   const int team = kForm == kSplit ? (int)parts : kG;                   // CTAs of a worker
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     ptx::mbar_init(drain, 1);
     ptx::mbar_init(part_full, 8 * parts);
     ptx::mbar_init(part_free, 8 * parts);
-    if constexpr (kForm == kPair)
+    if constexpr (F::kPaired)
       for (int g = 0; g < (int)F::kTmemCols / F::kGran; ++g) ptx::mbar_init(col_free + g, 8);   // a set's warps, two CTAs
     *abort_flag = 0;
     ptx::fence_mbar_init();
@@ -212,11 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     r.row = row0 + (int64_t)chunk * each;
     return r;
   };
-  // kPair: of n columns from `at` on, those of the first MMA: up to the ring's
+  // Pairs: of n columns from `at` on, those of the first MMA: up to the ring's
   // end, and 256 at most. A second one takes the rest (288 or fewer are left
   // with 256 or fewer).
   auto first_columns = [](int at, int n) {
-    if (kForm != kPair) return n;
+    if (!F::kPaired) return n;
     const int to_end = (int)F::kTmemCols - at;
     return n < to_end ? (n < 256 ? n : 256) : (to_end < 256 ? to_end : 256);
   };
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     uint32_t armed = 0, armed_parity = 0;
     const uint64_t pol = ptx::policy_evict_first();   // kOne, kSplit: weights are read once
     bool ok = true;
-    int at = 0;   // kPair: the unit's first column
+    int at = 0;   // pairs: the unit's first column
     for (int u = worker; ok && u < units; u += workers) {
       const Unit j = unit(u);
       const int cols = columns(j.rows), c1 = first_columns(at, cols);
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     // ---------------------------------------------------------------- MMA issuer (CTA 0)
     if (rank == 0) {
       uint32_t stage = 0, phase = 0, i = 0;
-      uint32_t uses = 0;   // kPair: bit g: parity of the uses of columns 32 g ..
+      uint32_t uses = 0;   // pairs: bit g: parity of the uses of columns 32 g ..
       int at = 0;
       bool ok = true;
       for (int u = worker; ok && u < units; u += workers, ++i) {
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
         const int cols = columns(unit(u).rows), c1 = first_columns(at, cols);
         int good = 1;
         if (lane == 0) good = wait_bar(acc_empty + slot, use ^ 1u, abort_flag, p.hdr, 0x58000000u | slot);
-        if constexpr (kForm == kPair) {   // and the unit's columns are free, lane by lane
+        if constexpr (F::kPaired) {   // and the unit's columns are free, lane by lane
           constexpr int kGrans = (int)F::kTmemCols / F::kGran;
           const int g = (at / F::kGran + lane) % kGrans;
           const bool mine = lane < cols / F::kGran;
@@ -314,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
         }
         if (!__all_sync(0xffffffffu, good)) break;
         ptx::tc_fence_after();
-        const uint32_t d = tmem + (kForm == kPair ? (uint32_t)at : slot * F::kRows);
-        const uint32_t d2 = tmem + (uint32_t)((at + c1) % (int)F::kTmemCols);   // kPair: of the second MMA
+        const uint32_t d = tmem + (F::kPaired ? (uint32_t)at : slot * F::kRows);
+        const uint32_t d2 = tmem + (uint32_t)((at + c1) % (int)F::kTmemCols);   // pairs: of the second MMA
         const uint32_t idesc = ptx::idesc_i8(128 * kG, c1), idesc2 = ptx::idesc_i8(128 * kG, cols - c1);
         const uint64_t b2_off = (uint64_t)(c1 / kG * kSlab) >> 4;
         const bool two = c1 < cols;
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
               if constexpr (kG == 2) ptx::mma_i8_pair(d, a + 2 * kk, b + 2 * kk, idesc, k > k_first || kk ? 1u : 0u);
               else ptx::mma_i8(d, a + 2 * kk, b + 2 * kk, idesc, k > k_first || kk ? 1u : 0u);
             }
-            if (kForm == kPair && two) {
+            if (F::kPaired && two) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 ptx::mma_i8_pair(d2, a + 2 * kk, b + b2_off + 2 * kk, idesc2, k > k_first || kk ? 1u : 0u);
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
       return true;
     };
     uint32_t i = 0;
-    int at = 0;   // kPair: the unit's first column
+    int at = 0;   // pairs: the unit's first column
     for (int u = worker; u < units; u += workers, ++i) {
       const Unit j = unit(u);
       const uint32_t slot = i & 1u, use = (i >> 1) & 1u;
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
       while (!ptx::mbar_try_wait(acc_full + slot, use)) {}   // completed: returns at once
       ptx::tc_fence_after();
       const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-      const int d = kForm == kPair ? at : (int)slot * F::kRows;
+      const int d = F::kPaired ? at : (int)slot * F::kRows;
       at = (at + columns(j.rows)) % (int)F::kTmemCols;
       const int64_t tile0 = n0 - ch;   // the CTA's first channel
       // bf16: two lanes exchange half of their rows, so that each stores two
@@ -494,10 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
       };
       for (int c0 = 32 * set; c0 < j.rows; c0 += 64) {
         uint32_t v[32];
-        const int col = kForm == kPair ? (d + c0) % (int)F::kTmemCols : d + c0;
+        const int col = F::kPaired ? (d + c0) % (int)F::kTmemCols : d + c0;
         ptx::tmem_ld_x32(lanes + (uint32_t)col, v);
         ptx::tmem_wait_ld();
-        if constexpr (kForm == kPair) {   // the columns are in registers: give them back
+        if constexpr (F::kPaired) {   // the columns are in registers: give them back
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -657,15 +661,20 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a) {
     return launch_gemm_i8_few(a);
   const int64_t fill = a.d.fill > 0 && a.d.fill < a.d.M ? a.d.fill : a.d.M, E = a.d.experts;
   const int64_t nk = ceil_div(a.d.K, kSlab), ch = a.wu ? 64 : 128;
-  // units to expect: experts with rows, each of its share
-  const int64_t used = std::min(E, fill), share = ceil_div(fill, used);
+  // units to expect: experts with rows, each of its share, and in windows of what
+  // few exceed where every token picks its experts at random
+  const int64_t used = std::min(E, fill), even = ceil_div(fill, used);
+  const int64_t share = a.win.offsets ? even + (int64_t)(2.0 * std::sqrt((double)even)) : even;
   const int64_t pairs = used * ceil_div(share, 256) * ceil_div(a.d.N, 2 * ch);
   const int64_t ones = used * ceil_div(share, 64) * ceil_div(a.d.N, ch);
   // A pair takes 0.36 us a slab (a full chunk), a CTA 0.24 us: compare the
   // rounds of units. Measured, pairs / single CTAs: 200 x 4096 x 7168 28 / 18 us;
-  // 32 experts of gate/up 2048 x 7168, 64 rows each 180 / 164 us, 128 rows 186 / 234
+  // 32 experts of gate/up 2048 x 7168, 64 rows each 180 / 164 us, 128 rows 186 / 234.
+  // Chunks of 128 / 256 rows: 96 rows each 174 / 184 us, about 128 each 211 / 188
+  // (half of the experts then have two). Chunks of more than 256 where two rounds
+  // of units are full anyway.
   if (a.num_sms >= 2 && 3 * ceil_div(pairs, a.num_sms / 2) <= 2 * ceil_div(ones, a.num_sms))
-    return launch_form<kPair>(a, 2, pairs >= a.num_sms);   // wide chunks where two rounds are full anyway
+    return share <= 128 ? launch_form<kPair128>(a, 2) : launch_form<kPair>(a, 2, pairs >= a.num_sms);
   // A CTA takes 0.24 us a slab; sharing K over 2 or 4 costs 2 to 4 us. Measured,
   // 1 / 2 / 4 CTAs: one row, 4096 x 7168 17.2 / 12.3 / 9.9 us, 64 rows 18.0 /
   // 15.1 / 12.0; 7168 x 2048 7.6 / 7.6 us, 64 rows 8.2 / 10.2

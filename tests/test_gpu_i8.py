@@ -234,6 +234,7 @@ GROUPS = [
     dict(counts=[700], gap=1, N=320, K=528),
     dict(counts=[1] * 200 + [400], gap=0, N=48, K=96),
     dict(counts=[256, 257, 511, 33], gap=0, N=512, K=640),
+    dict(counts=[90, 100, 128, 129, 65, 3, 200, 70], gap=1, N=1500, K=272),
     # many units: chunks of up to 288 rows, which go around tensor memory in every way
     dict(counts=[270, 257, 288, 289, 300, 550, 560, 31, 0, 700, 230, 576], gap=3, N=2600, K=320),
 ]
