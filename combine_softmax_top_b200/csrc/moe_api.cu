@@ -384,6 +384,7 @@ namespace {
 moe_status check_gate(const moe_shape* s, const moe_gate_desc* g) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
+  if (s->T > INT32_MAX - 64) return MOE_ERR_INVALID_ARG;   // token indices of a last, partly filled block
   if (!g || (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID)) return MOE_ERR_INVALID_ARG;
   if (!is_dtype(g->logits_dtype)) return MOE_ERR_INVALID_ARG;
   if (g->logits_dtype == MOE_E4M3) return MOE_ERR_UNSUPPORTED;
@@ -457,7 +458,7 @@ moe_status moe_quant_i8(int64_t rows, int64_t cols, int32_t src_dtype, const voi
 moe_status moe_gemm_i8(const moe_gemm_i8_desc* d, const int8_t* x, const float* x_scale, const int8_t* w,
                        const float* w_scale, const int8_t* w_up, const float* up_scale, const int32_t* offsets,
                        const int32_t* counts, void* y, void* ws, moe_stream_t stream) {
-  if (!d || d->reserved != 0 || d->M < 0 || d->M > INT32_MAX || d->N < 1 || d->K < 16 || d->K > 131056 ||
+  if (!d || d->reserved != 0 || d->M < 0 || d->M > INT32_MAX - 511 || d->N < 1 || d->K < 16 || d->K > 131056 ||
       d->K % 16 != 0 || d->fill < 0 || d->experts < 1 || d->experts > 1024 || d->N > INT32_MAX / d->experts)
     return MOE_ERR_INVALID_ARG;
   if ((ceil_div(d->M, 64) + d->experts) > INT32_MAX / ceil_div(d->N, 64)) return MOE_ERR_INVALID_ARG;

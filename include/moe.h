@@ -452,7 +452,7 @@ typedef struct moe_gate_desc {
 /*
  * Routing by `gate`, an alternative to moe_route with the same outputs.
  *   shape    the layer (T, E, topk, renorm and MOE_FLAG_SHARED_EXPERT are used:
- *            with a shared expert the last slot is E with weight 1)
+ *            with a shared expert the last slot is E with weight 1; T < 2^31 - 64)
  *   logits   [T, E] gate->logits_dtype, device
  *   bias     [E] fp32, device, or NULL
  *   topk_idx [T, topk] int32, device (out)
@@ -520,7 +520,7 @@ MOE_API moe_status moe_quant_i8(int64_t rows, int64_t cols, int32_t src_dtype, c
                                 moe_stream_t stream);
 
 typedef struct moe_gemm_i8_desc {
-  int64_t M;         /* rows of x and y, 0 .. 2^31 - 1 */
+  int64_t M;         /* rows of x and y, 0 .. 2^31 - 512 */
   int64_t N;         /* output channels of one expert, >= 1; experts * N < 2^31,
                         and (M / 64 + experts) * N / 64, each rounded up, < 2^31 */
   int64_t K;         /* a multiple of 16, 16 .. 131056: the sums stay below 2^31 */

@@ -51,6 +51,10 @@ def test_gate_refuses_descriptions(over, code):
 def test_gate_refuses_shapes_and_pointers():
     assert _call_gate(_shape(), None) == INVALID
     assert _call_gate(_shape(topk=0), _gate()) == INVALID
+    most = moe.make_shape(W.spec("sweep", T=(1 << 31) - 60, H=128, E=1, k=1, xq=W.BF16, compact=0))
+    most.cap_rows = 128
+    one = _gate(groups=1, topk_groups=1, group_best=1)
+    assert _call_gate(most, one) == INVALID and _call_back(most, one) == INVALID
     # 4 open groups of 8 experts hold 32, one open group 8
     assert _call_gate(_shape(topk=9), _gate(topk_groups=1)) == INVALID
     assert _call_back(_shape(topk=9), _gate(topk_groups=1)) == INVALID
@@ -90,7 +94,7 @@ def _gemm(M=4, N=128, K=128, experts=1, fill=0, out=moe.MOE_BF16, reserved=0, x=
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(M=(1 << 31) - 1, N=1 << 12), INVALID),
+    (dict(M=(1 << 31) - 1, N=1 << 12), INVALID), (dict(M=(1 << 31) - 511, N=1), INVALID),
     (dict(M=-1), INVALID), (dict(M=1 << 31), INVALID), (dict(N=0), INVALID), (dict(N=1 << 31), INVALID),
     (dict(K=0), INVALID), (dict(K=24), INVALID), (dict(K=131072), INVALID), (dict(fill=-1), INVALID),
     (dict(reserved=1), INVALID), (dict(out=moe.MOE_E4M3), UNSUPPORTED), (dict(out=11), INVALID),
