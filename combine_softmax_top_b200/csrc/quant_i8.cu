@@ -197,7 +197,9 @@ quant_i8_kernel(const T* __restrict__ x, int64_t rows, int cols, RowWindows win,
 template <typename T, int kTeam, int kKeep>
 cudaError_t go(int64_t rows, int64_t cols, const void* x, const RowWindows& win, int8_t* q, float* scale, int num_sms,
                cudaStream_t stream) {
-  const int64_t need = ceil_div(rows, kThreads / kTeam), most = 16 * (int64_t)num_sms;
+  // as many blocks as are resident where each first has to add up the windows
+  // (1024 rows in 256 windows: 9.9 us with twice as many, 7.8 us)
+  const int64_t need = ceil_div(rows, kThreads / kTeam), most = (win.offsets ? 8 : 16) * (int64_t)num_sms;
   quant_i8_kernel<T, kTeam, kKeep>
       <<<(unsigned)(need < most ? need : most), kThreads, 0, stream>>>((const T*)x, rows, (int)cols, win, q, scale);
   return cudaGetLastError();
