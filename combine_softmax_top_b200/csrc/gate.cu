@@ -26,9 +26,9 @@
 //
 // gate_backward_kernel writes what every expert gets (zero, or -p_e dot for a
 // plain softmax) 16 bytes a lane, then the chosen experts' derivatives over it.
-// The row is read only for a plain softmax. 8192 x 256 f32, renormalised: 3.5 us
-// (2.6 TB/s); 32768 x 128 bf16, plain softmax, 7.9 us (2.4 TB/s, bound by the two
-// exponentials an element).
+// The row is read only for a plain softmax, once where registers hold it. 8192 x
+// 256 f32, renormalised: 3.5 us (2.6 TB/s); 32768 x 128 bf16, plain softmax, 5.2 us
+// (3.6 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -553,8 +553,9 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
 }
 
 // S lanes a token (topk <= S). Elements go kW at a time, 16 bytes where rows
-// start on such a boundary, else one.
-template <typename T, bool kSigmoid, bool kRenorm, int S, int kW>
+// start on such a boundary, else one. With NV > 0 a plain softmax keeps its row in
+// NV registers a lane (E <= S NV): one exponential an element instead of two.
+template <typename T, bool kSigmoid, bool kRenorm, int S, int kW, int NV>
 __global__ void __launch_bounds__(kWarps * 32)
 gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ topk_idx,
                      const float* __restrict__ grad_w, int tokens, int E, int k, int shared, float scale,
@@ -578,7 +579,29 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
   if (live) l = load_logit(row + e);
   else gw = 0.f;
   float top = 0.f, inv = 0.f, dot = 0.f;
-  if constexpr (kEvery) {
+  float p[NV > 0 ? NV : 1];
+  if constexpr (kEvery && NV > 0) {
+#pragma unroll
+    for (int c = 0; c < NV; c += kW) {
+      float v[kW];
+      const int i = li * kW + c * S;
+      if (i < E) load_vec<kW>(row + i, v);
+#pragma unroll
+      for (int b = 0; b < kW; ++b) p[c + b] = i < E ? v[b] : -INFINITY;
+    }
+    top = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) top = fmaxf(top, p[c]);
+    top = sub_max<S>(top);
+    float z = 0.f;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      p[c] = p[c] == -INFINITY ? 0.f : __expf(p[c] - top);
+      z += p[c];
+    }
+    inv = 1.f / sub_sum<S>(z);
+    dot = sub_sum<S>(live ? gw * (expf(l - top) * inv) : 0.f);
+  } else if constexpr (kEvery) {
     // running maximum and sum in one pass
     float m = -INFINITY, z = 0.f;
     for (int i = li * kW; i < E; i += S * kW) {
@@ -600,7 +623,15 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
     dot = sub_sum<S>(live ? gw * (expf(l - top) * inv) : 0.f);
   }
   // what every expert gets
-  if (real) {
+  if (kEvery && NV > 0) {
+#pragma unroll
+    for (int c = 0; c < NV; c += kW) {
+      float v[kW];
+#pragma unroll
+      for (int b = 0; b < kW; ++b) v[b] = p[kEvery && NV > 0 ? c + b : 0] * inv * -dot;
+      if (real && li * kW + c * S < E) store_vec<kW>(grow + li * kW + c * S, v);
+    }
+  } else if (real) {
     for (int i = li * kW; i < E; i += S * kW) {
       float v[kW];
       if constexpr (kEvery) {
@@ -631,7 +662,7 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
   }
   // an expert named twice: every slot of it writes their sum, in slot order
   bool twice = false;
-#pragma unroll 1
+#pragma unroll 7
   for (int off = 1; off < S; ++off) {
     const int o = __shfl_xor_sync(kFull, live ? e : -1, off);
     twice |= live && o == e;
@@ -701,12 +732,19 @@ cudaError_t launch_gate_backward(const moe_shape& s, const moe_gate_desc& g, con
     constexpr bool kSig = decltype(sig)::value, kRen = decltype(ren)::value;
     constexpr int kV = 16 / sizeof(L);
     // the fewest lanes that hold the slots: 8 against 32 lanes 8192 x 256 f32
-    // 3.5 / 6.3 us, one token 2.1 / 3.0
+    // 3.5 / 6.3 us, one token 2.1 / 3.0. A plain softmax keeps its row in registers
+    // (against reading it twice 32768 x 128 bf16 5.2 / 7.9 us, 32768 x 1024 32 / 44)
+    if constexpr (!kSig && !kRen) {
+      if (E % kV == 0 && k <= 8 && E <= 128) return go(gate_backward_kernel<L, kSig, kRen, 8, kV, 16>, l, d, 8);
+      if (E % kV == 0 && k <= 8 && E <= 256) return go(gate_backward_kernel<L, kSig, kRen, 8, kV, 32>, l, d, 8);
+      if (E % kV == 0 && E <= 512) return go(gate_backward_kernel<L, kSig, kRen, 32, kV, 16>, l, d, 32);
+      if (E % kV == 0) return go(gate_backward_kernel<L, kSig, kRen, 32, kV, 32>, l, d, 32);
+    }
     if (k <= 8)
-      return E % kV == 0 ? go(gate_backward_kernel<L, kSig, kRen, 8, kV>, l, d, 8)
-                         : go(gate_backward_kernel<L, kSig, kRen, 8, 1>, l, d, 8);
-    return E % kV == 0 ? go(gate_backward_kernel<L, kSig, kRen, 32, kV>, l, d, 32)
-                       : go(gate_backward_kernel<L, kSig, kRen, 32, 1>, l, d, 32);
+      return E % kV == 0 ? go(gate_backward_kernel<L, kSig, kRen, 8, kV, 0>, l, d, 8)
+                         : go(gate_backward_kernel<L, kSig, kRen, 8, 1, 0>, l, d, 8);
+    return E % kV == 0 ? go(gate_backward_kernel<L, kSig, kRen, 32, kV, 0>, l, d, 32)
+                       : go(gate_backward_kernel<L, kSig, kRen, 32, 1, 0>, l, d, 32);
   };
   auto by_form = [&](auto* l, auto* d) {
     std::true_type yes;

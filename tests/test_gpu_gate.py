@@ -121,6 +121,15 @@ FORMS = [
     dict(E=1, k=1, score="sigmoid", renorm=0),
     dict(E=2, k=2, groups=2, topk_groups=2),
     dict(E=512, k=10, groups=1, topk_groups=1, best=2, bias=True),
+    # plain softmax: the gradient's row in registers, a quarter warp or a warp a token
+    dict(E=128, k=8, renorm=0, dtype=W.BF16),
+    dict(E=200, k=3, renorm=0, scale=2.0),
+    dict(E=256, k=8, renorm=0, dtype=W.BF16, bias=True),
+    dict(E=384, k=8, renorm=0, dtype=W.BF16),
+    dict(E=1024, k=8, renorm=0),
+    dict(E=516, k=12, renorm=0),
+    dict(E=1000, k=7, renorm=0, dtype=W.BF16),
+    dict(E=1002, k=7, renorm=0, dtype=W.BF16),
 ]
 
 
