@@ -352,6 +352,8 @@ def _windows(fn, offsets, counts, dev):
     if offsets is None and counts is None:
         return 0, None, None
     n = 0 if offsets is None else offsets.numel()
+    if n == 0:   # no windows: their null address would read as all rows
+        raise ValueError(f"{fn}: offsets must be a tensor of at least one window, next to counts")
     return n, _dense(fn, "offsets", offsets, (n,), _I32, dev), _dense(fn, "counts", counts, (n,), _I32, dev)
 
 

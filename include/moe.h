@@ -505,7 +505,7 @@ MOE_API moe_status moe_gate_backward(const moe_shape* shape, const moe_gate_desc
  *   q[r, k]  = x[r, k] / scale[r], rounded to nearest, ties to even
  * the reciprocal, the product and the quotient correctly rounded in binary32,
  * so q is the same everywhere.
- *   rows, cols  >= 0; cols a multiple of 16, at most 2^24
+ *   rows, cols  >= 0; cols a multiple of 16, at most 2^24; with 0 of either nothing is written
  *   src_dtype   MOE_F32 or MOE_BF16
  *   x           [rows, cols] src_dtype, device
  *   experts, offsets, counts  windows ([experts] int32, device), or 0, NULL, NULL

@@ -154,6 +154,22 @@ def test_quant_nothing_to_do():
     assert (s == -5).all()
 
 
+def test_no_windows_are_not_all_rows(ws):
+    """Empty offsets and counts have no address; they are refused, not read as
+    a call without windows."""
+    x = torch.ones(4, 128, device="cuda")
+    q, s = torch.full((4, 128), 99, dtype=torch.int8, device="cuda"), torch.full((4,), -5.0, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = torch.full((4, 128), -5.0, device="cuda")
+    for o, c in ((none, none), (none, one), (one, none), (None, one), (one, None)):
+        with pytest.raises(ValueError, match="offsets|counts"):
+            moe.moe_quant_i8(x, q, s, offsets=o, counts=c)
+        with pytest.raises(ValueError, match="offsets|counts|windows"):
+            moe.moe_gemm_i8(q, s, q, s, y, ws, offsets=o, counts=c)
+    assert (q == 99).all() and (s == -5).all() and (y == -5).all()
+
+
 # ---------------------------------------------------------------- products --
 
 def ints(shape, seed, full=False):
