@@ -45,7 +45,7 @@ constexpr uint32_t kLeastKey = 0x00800000u;   // of the lowest number; -infinity
 // 32-bit key that orders like the number
 __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t b = __float_as_uint(f + 0.f);   // -0 and +0 are one value
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
 template <typename T>
@@ -118,9 +118,15 @@ __device__ __forceinline__ V sub_sum(V v) {
 }
 template <int S>
 __device__ __forceinline__ float sub_max(float v) {
+  if constexpr (S == 32) {   // a NaN gives way to a number, as in fmaxf
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+  } else {
 #pragma unroll
-  for (int off = S / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
-  return v;
+    for (int off = S / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+    return v;
+  }
 }
 template <int S>
 __device__ __forceinline__ uint32_t sub_max(uint32_t v) {
@@ -164,8 +170,7 @@ __device__ __forceinline__ float renorm_term(float l, bool live) {
   const float top = sub_max<S>(live ? l : -INFINITY);
   if (!live) return 0.f;
   if (!kSigmoid) return expf(l - top);
-  const float m = fminf(top, 0.f);
-  return l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - m) / (1.f + expf(l));
+  return (l > 0.f ? 1.f : expf(l - fminf(top, 0.f))) / (1.f + expf(-fabsf(l)));
 }
 
 // 64-bit key that orders like the number
@@ -410,23 +415,26 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     const float e = two ? 2.f * err0 + err1 * (fabsf(b1) + fabsf(b2)) + 0x1p-23f * fabsf(r)
                         : (scores ? err0 + err1 * fabsf(b1) : 0.f);
     const float lo = r - e, hi = r + e;
-    // a group is open if fewer than topk_groups others may be above it
+    // a group is open if fewer than topk_groups others may be above it; its lanes
+    // share the comparisons
     const int step = gr.span ? gr.span : 1;
     int above = 0, may = 0;
-    if (scores) {
-      for (int h = 0; h < g.groups; ++h) {
-        const float olo = __shfl_sync(kFull, lo, base + h * step), ohi = __shfl_sync(kFull, hi, base + h * step);
-        above += olo > hi;       // not of itself
-        may += !(ohi < lo);      // of itself too
+    for (int h0 = 0; h0 < g.groups; h0 += step) {
+      const int h = h0 + (li & (step - 1)), src = base + h * step;
+      if (scores) {
+        const float olo = __shfl_sync(kFull, lo, src), ohi = __shfl_sync(kFull, hi, src);
+        above += h < g.groups && olo > hi;       // not of itself
+        may += h < g.groups && !(ohi < lo);      // of itself too
+      } else {   // exact: ties to the lowest group
+        const float o = __shfl_sync(kFull, r, src);
+        above += h < g.groups && (o > r || (o == r && h < gi));
       }
-      --may;
-    } else {   // exact: ties to the lowest group
-      for (int h = 0; h < g.groups; ++h) {
-        const float o = __shfl_sync(kFull, r, base + h * step);
-        above += o > r || (o == r && h < gi);
-      }
-      may = above;
     }
+    for (int off = 1; off < step; off <<= 1) {
+      above += __shfl_xor_sync(kFull, above, off);
+      may += __shfl_xor_sync(kFull, may, off);
+    }
+    may = scores ? may - 1 : above;
     const bool in = gi < g.groups;
     unsure = in && may >= g.topk_groups && above < g.topk_groups;
     const uint32_t opens = __ballot_sync(kFull, in && may < g.topk_groups) >> base;
@@ -452,17 +460,26 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
 #pragma unroll
   for (int v = 0; v < NV; ++v) key[v] = (order_key(c[v]) & ~kIdx) | (kIdx - (uint32_t)(e0 + v));
   sort_descending<0, NV>(key);
+  // the two largest stay in registers, the others wait in shared memory, two
+  // kNoKey behind them (a lane's list is popped NV times at most)
+  uint32_t* list = reinterpret_cast<uint32_t*>(scratch) + lane * (NV + 4);
+#pragma unroll
+  for (int v = 0; v < NV; v += 4)
+    *reinterpret_cast<uint4*>(list + v) = make_uint4(key[v], key[v + 1], key[v + 2], key[v + 3]);
+  *reinterpret_cast<uint2*>(list + NV) = make_uint2(kNoKey, kNoKey);
+  uint32_t head = key[0], second = key[1];
+  list += 2;
   uint32_t won = kNoKey;   // lane j: slot j's key (lane k: that of the best one left)
   auto pop = [&](uint32_t m, int j) {   // the largest head m, into lane j
     won = li == j ? m : won;
-    const bool win = key[0] == m;
-#pragma unroll
-    for (int v = 0; v + 1 < NV; ++v) key[v] = win ? key[v + 1] : key[v];
-    key[NV - 1] = win ? kNoKey : key[NV - 1];
+    if (head == m) {
+      head = second;
+      second = *list++;
+    }
   };
   const int rounds = lossless ? k : min(k + 1, S);
 #pragma unroll 1
-  for (int j = 0; j < rounds; ++j) pop(sub_max<S>(key[0]), j);
+  for (int j = 0; j < rounds; ++j) pop(sub_max<S>(head), j);
   int sel = won < kLeastKey ? -1 : (int)(kIdx - (won & kIdx));
   float lj = sel >= 0 ? load_logit(row + sel) : 0.f;
   unsure = sub_any<S>(unsure) && !dead;   // which groups are open
@@ -482,13 +499,13 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
       // pop whatever may reach the last slot
       const uint32_t lim = order_key(__shfl_sync(kFull, v - (near + cut), base + k - 1));
       int n = rounds;
-      uint32_t m = sub_max<S>(key[0]);
+      uint32_t m = sub_max<S>(head);
       auto reaches = [&]() { return doubt && m >= kLeastKey && (m | kIdx) >= lim; };
       while (__any_sync(kFull, reaches() && n < S)) {
         const bool take = reaches() && n < S;
         pop(take ? m : ~0u, take ? n : -1);   // ~0 is no key: nothing is taken
         n += take;
-        m = sub_max<S>(key[0]);
+        m = sub_max<S>(head);
       }
       unsure = unsure || reaches();   // more candidates than lanes
       const int cand = won < kLeastKey ? -1 : (int)(kIdx - (won & kIdx));
@@ -515,7 +532,10 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
       __syncwarp();
       if (doubt && cand >= 0 && rank < k) slots[rank] = cand;
       __syncwarp();
-      if (doubt && !unsure && li < k) sel = slots[li];
+      if (doubt && !unsure && li < k) {
+        sel = slots[li];
+        lj = load_logit(row + sel);
+      }
     }
   }
   uint32_t again = __ballot_sync(kFull, unsure);
@@ -526,16 +546,18 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     const int s = choose_exactly<T, kSigmoid>(logits + (int64_t)__shfl_sync(kFull, t, first) * E, bias, E, k, gr.n,
                                               g, __shfl_sync(kFull, top, first), scratch);
     const int got = __shfl_sync(kFull, s, li);
-    if (base == first && li < k) sel = got;
+    if (base == first && li < k) {
+      sel = got;
+      lj = load_logit(row + sel);
+    }
     __syncwarp();
   }
 
   const bool live = li < k;
-  lj = live && sel >= 0 ? load_logit(row + sel) : 0.f;   // -1 in a dead row only
   float a;
   if (renorm) {
     a = renorm_term<kSigmoid, S>(lj, live);
-    a /= sub_sum<S>(a);
+    a /= k <= 8 ? sub_sum<8>(a) : sub_sum<S>(a);   // of the slots' lanes
   } else {
     a = kSigmoid ? 1.f / (1.f + expf(-lj)) : expf(lj - top) / z;
   }
@@ -686,10 +708,10 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
 cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits, const float* bias, int32_t* idx,
                         float* w) {
   const int T = (int)c.s.T, E = (int)c.routed_E, k = (int)c.routed_k;
-  auto go = [&](auto kernel, auto* l, int S) {
+  auto go = [&](auto kernel, auto* l, int S, int NV) {
     const int per = (E + S - 1) / S, tokens = kWarps * 32 / S;   // tokens of a block
-    // a warp's scratch in doubles: a row, the tokens' rows in floats, 32 slots
-    Groups gr{E / g.groups, 0, std::max(std::max(E, (32 / S * E + 1) / 2), 16)};
+    // a warp's scratch in doubles: a row, the tokens' rows in floats, the lanes' lists
+    Groups gr{E / g.groups, 0, std::max(std::max(E, (32 / S * E + 1) / 2), 16 * (NV + 4)) + 1 & ~1};
     if (gr.n % per == 0 && ((gr.n / per) & (gr.n / per - 1)) == 0) gr.span = gr.n / per;
     kernel<<<(T + tokens - 1) / tokens, kWarps * 32, (size_t)kWarps * gr.scratch * sizeof(double), c.stream>>>(
         l, bias, T, E, per, k, c.shared, c.s.renorm, g, gr, idx, w, c.ws.hdr);
@@ -705,13 +727,13 @@ cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits
     // 8192 x 64 f32 6.5 / 5.5, 4096 4.6 / 4.6; 16384 x 256 f32 with bias and groups
     // 17.2 / 16.4, 8192 10.6 / 11.0
     if (T >= 4096 && lanes <= 8 && E <= 128)
-      return E <= 64 ? go(gate_kernel<L, kSig, 8, 8>, l, 8) : go(gate_kernel<L, kSig, 16, 8>, l, 8);
+      return E <= 64 ? go(gate_kernel<L, kSig, 8, 8>, l, 8, 8) : go(gate_kernel<L, kSig, 16, 8>, l, 8, 16);
     if (T >= (E <= 128 ? 8192 : 12288) && lanes <= 16 && E <= 256)
-      return E <= 128 ? go(gate_kernel<L, kSig, 8, 16>, l, 16) : go(gate_kernel<L, kSig, 16, 16>, l, 16);
-    if (E <= 128) return go(gate_kernel<L, kSig, 4, 32>, l, 32);
-    if (E <= 256) return go(gate_kernel<L, kSig, 8, 32>, l, 32);
-    if (E <= 512) return go(gate_kernel<L, kSig, 16, 32>, l, 32);
-    return go(gate_kernel<L, kSig, 32, 32>, l, 32);
+      return E <= 128 ? go(gate_kernel<L, kSig, 8, 16>, l, 16, 8) : go(gate_kernel<L, kSig, 16, 16>, l, 16, 16);
+    if (E <= 128) return go(gate_kernel<L, kSig, 4, 32>, l, 32, 4);
+    if (E <= 256) return go(gate_kernel<L, kSig, 8, 32>, l, 32, 8);
+    if (E <= 512) return go(gate_kernel<L, kSig, 16, 32>, l, 32, 16);
+    return go(gate_kernel<L, kSig, 32, 32>, l, 32, 32);
   };
   auto by_score = [&](auto* l) {
     return g.score == MOE_SCORE_SIGMOID ? by_size(l, std::true_type()) : by_size(l, std::false_type());
