@@ -33,6 +33,7 @@
 #include <type_traits>
 
 #include "moe_internal.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -42,9 +43,9 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kNoKey = 0u;
 constexpr uint32_t kLeastKey = 0x00800000u;   // of the lowest number; -infinity's is below
 
-// 32-bit key that orders like the number
+// 32-bit key that orders like the number, -0 below +0
 __device__ __forceinline__ uint32_t order_key(float f) {
-  const uint32_t b = __float_as_uint(f + 0.f);   // -0 and +0 are one value
+  const uint32_t b = __float_as_uint(f);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
@@ -146,13 +147,15 @@ __device__ __forceinline__ bool sub_any(bool p) {
   return ((all >> ((threadIdx.x & 31) / S * S)) & ((1u << (S & 31)) - 1u)) != 0u;
 }
 
-// exp for the choice: off by (4 + 1.5 |x|) 2^-24 relative at most (ex2.approx:
-// 2^-22; its argument is rounded twice, 2^-24 |x| / ln 2 each with a factor ln 2)
-__device__ __forceinline__ float quick_exp(float x) {
+constexpr float kLog2E = 1.4426950408889634f;
+__device__ __forceinline__ float quick_exp2(float x) {
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// exp for the choice: off by (4 + 1.5 |x|) 2^-24 relative at most (ex2.approx:
+// 2^-22; its argument is rounded twice, 2^-24 |x| / ln 2 each with a factor ln 2)
+__device__ __forceinline__ float quick_exp(float x) { return quick_exp2(x * kLog2E); }
 // 1 / x, x >= 1 (0 for infinity): off by 2^-23 relative at most
 __device__ __forceinline__ float quick_rcp(float x) {
   float r;
@@ -336,10 +339,16 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
 #pragma unroll
     for (int v = 0; v < NV; ++v) c[v] = 0.f;
   }
-  float zero = 0.f;   // stays 0 unless a value is not finite
+  uint64_t zeros = 0;   // two zeros, which stay that unless a value is not finite
+  auto check = [&](const float (&x)[NV]) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) zero = __fmaf_rn(l[v], 0.f, __fmaf_rn(c[v], 0.f, zero));
-  const bool dead = sub_any<S>(zero != 0.f);
+    for (int v = 0; v < NV; v += 2) zeros = ptx::fma2(ptx::two(x[v], x[v + 1]), 0ull, zeros);
+  };
+  check(l);
+  if (bias) check(c);
+  float zero, zero1;
+  ptx::split(zeros, zero, zero1);
+  const bool dead = sub_any<S>(zero + zero1 != 0.f);
   if (dead) {   // goes along as a row of zeros
 #pragma unroll
     for (int v = 0; v < NV; ++v) l[v] = c[v] = 0.f;
@@ -374,12 +383,26 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
   // bias: 2^-24 |c|.
   const float err0 = scores ? (kSigmoid ? 5.f * 0x1p-24f : 0x1p-17f * inv_z) : 0.f;
   const float err1 = bias ? 0x1p-23f : 0.f;
+  auto logits_choose = [&]() {   // -0 and +0 are one value
+#pragma unroll
+    for (int v = 0; v < NV; v += 2) ptx::split(ptx::add2(ptx::two(l[v], l[v + 1]), 0ull), c[v], c[v + 1]);
+  };
   if (scores) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) c[v] += quick_score<kSigmoid>(l[v], top, inv_z);
+    for (int v = 0; v < NV; v += 2) {   // quick_score, two at a time
+      const uint64_t x = ptx::two(l[v], l[v + 1]), b = ptx::two(c[v], c[v + 1]);
+      float p, q;
+      if (kSigmoid) {
+        ptx::split(ptx::mul2(x, ptx::two(-kLog2E, -kLog2E)), p, q);
+        ptx::split(ptx::add2(ptx::two(quick_exp2(p), quick_exp2(q)), ptx::two(1.f, 1.f)), p, q);
+        ptx::split(ptx::add2(ptx::two(quick_rcp(p), quick_rcp(q)), b), c[v], c[v + 1]);
+      } else {
+        ptx::split(ptx::mul2(ptx::add2(x, ptx::two(-top, -top)), ptx::two(kLog2E, kLog2E)), p, q);
+        ptx::split(ptx::fma2(ptx::two(quick_exp2(p), quick_exp2(q)), ptx::two(inv_z, inv_z), b), c[v], c[v + 1]);
+      }
+    }
   } else {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) c[v] = l[v];
+    logits_choose();
   }
 
   // groups: the slots of closed ones go below all others
@@ -438,10 +461,7 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     const bool in = gi < g.groups;
     unsure = in && may >= g.topk_groups && above < g.topk_groups;
     const uint32_t opens = __ballot_sync(kFull, in && may < g.topk_groups) >> base;
-    if (!bias && scores) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) c[v] = l[v];   // the scores only ranked the groups
-    }
+    if (!bias && scores) logits_choose();   // the scores only ranked the groups
     if (gr.span) {
       const bool open = may < g.topk_groups;
 #pragma unroll
@@ -497,7 +517,7 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     doubt = sub_any<S>(doubt) && !dead && !unsure;
     if (__any_sync(kFull, doubt)) {
       // pop whatever may reach the last slot
-      const uint32_t lim = order_key(__shfl_sync(kFull, v - (near + cut), base + k - 1));
+      const uint32_t lim = order_key(__shfl_sync(kFull, v - (near + cut), base + k - 1) + 0.f);
       int n = rounds;
       uint32_t m = sub_max<S>(head);
       auto reaches = [&]() { return doubt && m >= kLeastKey && (m | kIdx) >= lim; };

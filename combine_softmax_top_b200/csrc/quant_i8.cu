@@ -18,34 +18,13 @@
 // numbers are scaled by 2^64 first, which changes no quotient. Adding
 // 1.5 * 2^23 rounds to an integer, ties to even, whose low byte is the code.
 #include "moe_internal.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 128;
 constexpr int kMaxExperts = 1024;
-
-// Two binary32 numbers an instruction, each rounded to nearest as one alone.
-__device__ __forceinline__ uint64_t two(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
 // 16 bytes of consecutive elements, as loaded.
 template <typename T>
@@ -77,17 +56,17 @@ struct Piece {
   }
   template <bool kTiny>
   __device__ __forceinline__ void quantise(float s, float y, int8_t* q) const {
-    const uint64_t y2 = two(y, y), minus_s = two(-s, -s), magic = two(12582912.f, 12582912.f);   // 1.5 * 2^23
+    const uint64_t y2 = ptx::two(y, y), minus_s = ptx::two(-s, -s), magic = ptx::two(12582912.f, 12582912.f);   // 1.5 * 2^23
     float t[kN];
 #pragma unroll
     for (int i = 0; i < kN; i += 2) {   // two elements an instruction
-      uint64_t x = two(at(i), at(i + 1));
-      if (kTiny) x = mul2(x, two(0x1p64f, 0x1p64f));
-      uint64_t v = mul2(x, y2);
-      v = fma2(fma2(v, minus_s, x), y2, v);
-      v = fma2(fma2(v, minus_s, x), y2, v);
-      v = add2(v, magic);
-      asm("mov.b64 {%0, %1}, %2;" : "=f"(t[i]), "=f"(t[i + 1]) : "l"(v));
+      uint64_t x = ptx::two(at(i), at(i + 1));
+      if (kTiny) x = ptx::mul2(x, ptx::two(0x1p64f, 0x1p64f));
+      uint64_t v = ptx::mul2(x, y2);
+      v = ptx::fma2(ptx::fma2(v, minus_s, x), y2, v);
+      v = ptx::fma2(ptx::fma2(v, minus_s, x), y2, v);
+      v = ptx::add2(v, magic);
+      ptx::split(v, t[i], t[i + 1]);
     }
     uint32_t b[kN / 4];
 #pragma unroll
