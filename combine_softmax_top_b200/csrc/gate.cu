@@ -518,13 +518,14 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     if (__any_sync(kFull, doubt)) {
       // pop whatever may reach the last slot
       const uint32_t lim = order_key(__shfl_sync(kFull, v - (near + cut), base + k - 1) + 0.f);
-      int n = rounds;
+      int n = rounds, most = rounds;   // popped of this token, and of any here
       uint32_t m = sub_max<S>(head);
       auto reaches = [&]() { return doubt && m >= kLeastKey && (m | kIdx) >= lim; };
       while (__any_sync(kFull, reaches() && n < S)) {
         const bool take = reaches() && n < S;
         pop(take ? m : ~0u, take ? n : -1);   // ~0 is no key: nothing is taken
         n += take;
+        ++most;
         m = sub_max<S>(head);
       }
       unsure = unsure || reaches();   // more candidates than lanes
@@ -543,7 +544,7 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
                     : (kSigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top) / zd) + (double)__ldg(bias + cand);
       }
       int rank = 0;
-      for (int i = 0; i < S; ++i) {
+      for (int i = 0; i < most; ++i) {
         const double o = __shfl_sync(kFull, c64, base + i);
         const int os = __shfl_sync(kFull, cand, base + i);
         rank += os >= 0 && (o > c64 || (o == c64 && os < cand));
