@@ -14,9 +14,10 @@
 // c = s + bias carries binary32 roundings, so the chosen values (and the best
 // one left) are compared once more with the bounds of both. Where two
 // neighbours are closer than that, every candidate that could still belong to
-// the topk is popped, one to a lane, and these are ordered in binary64; a token
-// with a group at the border of the open ones closer than that is done over in
-// binary64 (choose_exactly). Without a bias c is the logit itself; bf16 logits
+// the topk is popped, one to a lane, and these are ordered in binary64. Groups
+// at the border of the open ones closer than that are ranked in binary64, by
+// the experts that can be their best, before all else is done over; where groups
+// are no sets of lanes all of it is done in binary64 (choose_exactly). Without a bias c is the logit itself; bf16 logits
 // then lose nothing in the keys and need no second look.
 //
 // Bound by instruction issue for many tokens (815 warp instructions a token of
@@ -182,6 +183,31 @@ __device__ __forceinline__ uint64_t order_key(double f) {
   return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
 }
 
+// The two best choice values in binary64 of those of this lane's `mine` experts
+// that are in `mask` (bias or scores, never logits); row and bias from its first on.
+template <typename T, bool kSigmoid, int S>
+__device__ __noinline__ double2 best_exactly(const T* row, const float* bias, int mine, uint32_t mask, float top) {
+  double z = 1.0;
+  if (!kSigmoid) {
+    z = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < mine; ++i) z += exp((double)load_logit(row + i) - (double)top);
+    z = sub_sum<S>(z);
+  }
+  double b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll 1
+  for (; mask; mask &= mask - 1) {
+    const int i = __ffs(mask) - 1;
+    const double l = load_logit(row + i);
+    const double s = kSigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / z;
+    const double v = bias ? s + (double)__ldg(bias + i) : s;
+    b2 = fmax(b2, fmin(b1, v));
+    b1 = fmax(b1, v);
+  }
+  __syncwarp();
+  return make_double2(b1, b2);
+}
+
 // The choice in binary64, lane j < k returning slot j's expert. n: experts of a
 // group. c: E doubles of shared memory of this warp.
 template <typename T, bool kSigmoid>
@@ -192,9 +218,11 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
   double z = 1.0;
   if (!kSigmoid && (bias || ranks)) {
     z = 0.0;
+#pragma unroll 1
     for (int e = lane; e < E; e += 32) z += exp((double)load_logit(row + e) - (double)top);
     z = sub_sum<32>(z);
   }
+#pragma unroll 1
   for (int e = lane; e < E; e += 32) {
     const double l = load_logit(row + e);
     const double s = !bias && !ranks ? l : kSigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / z;
@@ -204,12 +232,21 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
   uint32_t open = kFull;
   if (g.groups > 1) {
     double b1 = -INFINITY, b2 = -INFINITY;
-    if (lane < g.groups) {
-      for (int i = 0; i < n; ++i) {
-        const double v = c[lane * n + i];
+    int share = 1;   // lanes of a group: lane h, h + 32 / share, ... look at group h
+    while (2 * share * g.groups <= 32) share *= 2;
+    const int h = lane & (32 / share - 1);
+    if (h < g.groups) {
+#pragma unroll 4
+      for (int i = lane / (32 / share); i < n; i += share) {
+        const double v = c[h * n + i];
         b2 = fmax(b2, fmin(b1, v));
         b1 = fmax(b1, v);
       }
+    }
+    for (int off = 16; off >= 32 / share; off >>= 1) {
+      const double o1 = __shfl_xor_sync(kFull, b1, off), o2 = __shfl_xor_sync(kFull, b2, off);
+      b2 = fmax(fmax(b2, o2), fmin(b1, o1));
+      b1 = fmax(b1, o1);
     }
     const double r = g.group_best == 2 ? b1 + b2 : b1;
     int above = 0;
@@ -219,18 +256,21 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
     }
     open = __ballot_sync(kFull, lane < g.groups && above < g.topk_groups);
     __syncwarp();
-    for (int e = lane; e < E; e += 32) {   // each lane's own elements from here on
-      if (!((open >> (e / n)) & 1u)) c[e] = -INFINITY;
-      else if (ranks && !bias) c[e] = load_logit(row + e);
-    }
+  }
+  // keys in place of the values, 0 in closed groups; each lane's own from here on
+  for (int e = lane; e < E; e += 32) {
+    const bool in = g.groups == 1 || ((open >> (e / n)) & 1u);
+    const uint64_t key = in ? order_key(ranks && !bias ? (double)load_logit(row + e) : c[e]) : 0;
+    c[e] = __longlong_as_double((long long)key);
   }
   uint64_t best;
   int who;
   auto look = [&]() {   // this lane's largest, the lowest index of equals
     best = 0;
     who = INT32_MAX;
+#pragma unroll 4
     for (int e = lane; e < E; e += 32) {
-      const uint64_t q = order_key(c[e]);
+      const uint64_t q = (uint64_t)__double_as_longlong(c[e]);
       if (q > best) { best = q; who = e; }
     }
   };
@@ -243,7 +283,7 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
     const int e = (int)__reduce_min_sync(kFull, in && (uint32_t)best == lo ? (uint32_t)who : 0xFFFFFFFFu);
     if (lane == j) sel = e;
     if (who == e) {
-      c[e] = -INFINITY;
+      c[e] = __longlong_as_double(0);
       look();
     }
   }
@@ -287,9 +327,14 @@ __device__ __forceinline__ float quick_score(float l, float top, float inv_z) {
   return kSigmoid ? quick_rcp(1.f + quick_exp(-l)) : quick_exp(l - top) * inv_z;
 }
 
-// NV slots of a lane, the first `per` of them used; S lanes a token.
-template <typename T, bool kSigmoid, int NV, int S>
-__global__ void __launch_bounds__(kWarps * 32)
+// NV slots of a lane, the first `per` of them used; S lanes a token. kClose: there
+// are groups ranked by scores, and those too close to tell are ranked in binary64
+// before all else is done over. It costs registers (32768 x 160 with groups 24.3
+// us, 21.8 without) and spares choose_exactly (8192 x 256 with one such token 9.0
+// us, 12.1 without), so that it is for a warp a token, where few tokens do not
+// hide one that takes long.
+template <typename T, bool kSigmoid, int NV, int S, bool kClose>
+__global__ void __launch_bounds__(kWarps * 32, kClose && NV <= 8 ? 12 : 1)
 gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int tokens, int E, int per, int k,
             int shared, int renorm, moe_gate_desc g, Groups gr, int32_t* __restrict__ topk_idx,
             float* __restrict__ topk_w, Header* hdr) {
@@ -307,6 +352,8 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
   const int e0 = li * per;
   const int mine = max(0, min(per, E - e0));   // experts of this lane
 
+  uint32_t ranked = 0;   // kClose: open groups, once they had to be ranked in binary64 (never none)
+again:
   float l[NV], c[NV];   // logits, choice values
   // wide loads where every lane's part starts on a boundary and none is cut
   const bool wide = E == S * NV;
@@ -460,6 +507,37 @@ gate_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int to
     may = scores ? may - 1 : above;
     const bool in = gi < g.groups;
     unsure = in && may >= g.topk_groups && above < g.topk_groups;
+    if (kClose && ranked) {
+      may = (ranked >> (gi & 31)) & 1u ? 0 : g.topk_groups;
+      unsure = false;
+    } else if (kClose && gr.span && __any_sync(kFull, unsure && !dead)) {
+      // Too close to tell: from the values that can be a group's best two in
+      // binary64, then once more from the start, so that no registers wait
+      uint32_t mask = 0;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v < mine && !(c[v] < b2 - 4.f * (err0 + err1 * (fabsf(b2) + fabsf(c[v]))))) mask |= 1u << v;
+      double2 b = best_exactly<T, kSigmoid, S>(row + e0, bias ? bias + e0 : nullptr, mine, mask, top);
+      for (int off = 1; off < step; off <<= 1) {
+        const double o1 = __shfl_xor_sync(kFull, b.x, off), o2 = __shfl_xor_sync(kFull, b.y, off);
+        b.y = fmax(fmax(b.y, o2), fmin(b.x, o1));
+        b.x = fmax(b.x, o1);
+      }
+      const double rd = two ? b.x + b.y : b.x;
+      int over = 0;   // groups above, ties to the lowest
+#pragma unroll 1
+      for (int h = 0; h < g.groups; ++h) {
+        const double o = __shfl_sync(kFull, rd, base + h * step);
+        over += o > rd || (o == rd && h < gi);
+      }
+      const bool open = in && over < g.topk_groups;
+      ranked = 0;
+#pragma unroll 1
+      for (int h = 0; h < g.groups; ++h)
+        ranked |= (__shfl_sync(kFull, (int)open, base + h * step) ? 1u : 0u) << h;
+      if (dead || !ranked) ranked = kFull;
+      goto again;
+    }
     const uint32_t opens = __ballot_sync(kFull, in && may < g.topk_groups) >> base;
     if (!bias && scores) logits_choose();   // the scores only ranked the groups
     if (gr.span) {
@@ -738,9 +816,9 @@ cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits
         l, bias, T, E, per, k, c.shared, c.s.renorm, g, gr, idx, w, c.ws.hdr);
     return cudaGetLastError();
   };
-  auto by_size = [&](auto* l, auto sig) {
+  auto by_size = [&](auto* l, auto sig, auto close) {
     using L = std::remove_const_t<std::remove_pointer_t<decltype(l)>>;
-    constexpr bool kSig = decltype(sig)::value;
+    constexpr bool kSig = decltype(sig)::value, kClose = decltype(close)::value;
     // a lane for every slot and, where the keys are not exact, the best one left
     const int lanes = std::max(k + (sizeof(L) == 2 && !bias ? 0 : 1), (int)g.groups);
     // Fewer lanes a token once the SMs are full of warps anyway. Measured, warp
@@ -748,16 +826,20 @@ cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits
     // 8192 x 64 f32 6.5 / 5.5, 4096 4.6 / 4.6; 16384 x 256 f32 with bias and groups
     // 17.2 / 16.4, 8192 10.6 / 11.0
     if (T >= 4096 && lanes <= 8 && E <= 128)
-      return E <= 64 ? go(gate_kernel<L, kSig, 8, 8>, l, 8, 8) : go(gate_kernel<L, kSig, 16, 8>, l, 8, 16);
+      return E <= 64 ? go(gate_kernel<L, kSig, 8, 8, false>, l, 8, 8) : go(gate_kernel<L, kSig, 16, 8, false>, l, 8, 16);
     if (T >= (E <= 128 ? 8192 : 12288) && lanes <= 16 && E <= 256)
-      return E <= 128 ? go(gate_kernel<L, kSig, 8, 16>, l, 16, 8) : go(gate_kernel<L, kSig, 16, 16>, l, 16, 16);
-    if (E <= 128) return go(gate_kernel<L, kSig, 4, 32>, l, 32, 4);
-    if (E <= 256) return go(gate_kernel<L, kSig, 8, 32>, l, 32, 8);
-    if (E <= 512) return go(gate_kernel<L, kSig, 16, 32>, l, 32, 16);
-    return go(gate_kernel<L, kSig, 32, 32>, l, 32, 32);
+      return E <= 128 ? go(gate_kernel<L, kSig, 8, 16, false>, l, 16, 8) : go(gate_kernel<L, kSig, 16, 16, false>, l, 16, 16);
+    if (E <= 128) return go(gate_kernel<L, kSig, 4, 32, kClose>, l, 32, 4);
+    if (E <= 256) return go(gate_kernel<L, kSig, 8, 32, kClose>, l, 32, 8);
+    if (E <= 512) return go(gate_kernel<L, kSig, 16, 32, kClose>, l, 32, 16);
+    return go(gate_kernel<L, kSig, 32, 32, kClose>, l, 32, 32);
   };
   auto by_score = [&](auto* l) {
-    return g.score == MOE_SCORE_SIGMOID ? by_size(l, std::true_type()) : by_size(l, std::false_type());
+    std::true_type yes;
+    std::false_type no;
+    const bool close = g.groups > 1 && (bias || g.group_best == 2);
+    if (g.score == MOE_SCORE_SIGMOID) return close ? by_size(l, yes, yes) : by_size(l, yes, no);
+    return close ? by_size(l, no, yes) : by_size(l, no, no);
   };
   return g.logits_dtype == MOE_BF16 ? by_score((const __nv_bfloat16*)logits) : by_score((const float*)logits);
 }
