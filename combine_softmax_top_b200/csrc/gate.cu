@@ -8,22 +8,24 @@
 // keys that order like its choice values c, their low 6 to 10 bits given to the
 // expert (a sorting network of min and max, two instructions a comparison), and
 // each of the topk rounds takes the largest head with one reduction, which
-// names the expert too, and pops it.
+// names the expert too, and pops it (two heads in registers, the rest of a list in
+// shared memory: 32768 x 128 bf16 8.5 us, all in registers 10.1).
 //
 // What is chosen has to be what binary64 chooses. The keys drop low bits and
 // c = s + bias carries binary32 roundings, so the chosen values (and the best
 // one left) are compared once more with the bounds of both. Where two
 // neighbours are closer than that, every candidate that could still belong to
 // the topk is popped, one to a lane, and these are ordered in binary64. Groups
-// at the border of the open ones closer than that are ranked in binary64, by
-// the experts that can be their best, before all else is done over; where groups
-// are no sets of lanes all of it is done in binary64 (choose_exactly). Without a bias c is the logit itself; bf16 logits
-// then lose nothing in the keys and need no second look.
+// at the border of the open ones closer than that are ranked in binary64, by the
+// experts that can be their best, and all else is done over (few tokens, kClose),
+// or the token is chosen in binary64 altogether (choose_exactly). Without a bias
+// c is the logit itself; bf16 logits then lose nothing in the keys and need no
+// second look.
 //
-// Bound by instruction issue for many tokens (815 warp instructions a token of
-// 256 f32 logits with a bias and groups, 191 of 128 bf16 ones), by latency for
-// few: one token 2.7 us, 8192 x 256 f32 10.7 us, 32768 x 128 bf16 10.2 us
-// (0.8 and 0.9 TB/s of logits, where HBM would allow 6.5).
+// Bound by instruction issue for many tokens (709 warp instructions a token of
+// 256 f32 logits with a bias and groups, 143 of 128 bf16 ones), by latency for
+// few: one token 2.7 us, 8192 x 256 f32 8.7 us, 32768 x 128 bf16 8.1 us
+// (1.0 and 1.0 TB/s of logits, where HBM would allow 6.5).
 //
 // gate_backward_kernel writes what every expert gets (zero, or -p_e dot for a
 // plain softmax) 16 bytes a lane, then the chosen experts' derivatives over it.
@@ -822,9 +824,9 @@ cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits
     // a lane for every slot and, where the keys are not exact, the best one left
     const int lanes = std::max(k + (sizeof(L) == 2 && !bias ? 0 : 1), (int)g.groups);
     // Fewer lanes a token once the SMs are full of warps anyway. Measured, warp
-    // against part: 4096 x 128 bf16 3.7 / 3.4 us, 2048 the same, 512 2.5 / 3.0;
-    // 8192 x 64 f32 6.5 / 5.5, 4096 4.6 / 4.6; 16384 x 256 f32 with bias and groups
-    // 17.2 / 16.4, 8192 10.6 / 11.0
+    // against part: 6000 x 128 bf16 4.1 / 3.6 us, 4096 3.2 / 3.2, 2048 2.6 / 2.9;
+    // 8192 x 64 f32 5.4 / 4.9, 4096 3.8 / 4.2; 16384 x 160 bf16 with groups 12.3 /
+    // 11.4, 8192 7.2 / 6.9
     if (T >= 4096 && lanes <= 8 && E <= 128)
       return E <= 64 ? go(gate_kernel<L, kSig, 8, 8, false>, l, 8, 8) : go(gate_kernel<L, kSig, 16, 8, false>, l, 8, 16);
     if (T >= (E <= 128 ? 8192 : 12288) && lanes <= 16 && E <= 256)

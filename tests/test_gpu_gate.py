@@ -190,6 +190,41 @@ def test_few_candidates_at_a_border(score, near, T, k):
     check(c, l.cuda())
 
 
+@pytest.mark.parametrize("T", [1, 41, 16390])
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16])
+@pytest.mark.parametrize("score,bias", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+@pytest.mark.parametrize("E,G,Kg,k", [(256, 8, 4, 8), (96, 3, 1, 8), (160, 8, 3, 6), (128, 32, 5, 12), (1024, 16, 2, 8)])
+def test_groups_at_the_border_of_the_open_ones(E, G, Kg, k, score, bias, dtype, T):
+    """Some rows where the first closed group has the experts of the last open
+    one in another order, the best moved by one unit (a tie where the type has
+    no such unit); the others with groups far apart, one of them not finite."""
+    if T > 41 and E > 256:
+        T = 41
+    c = Case(T, E=E, k=k, score=score, dtype=dtype, bias=bias, groups=G, topk_groups=Kg, best=2)
+    flat = torch.full((E,), 0.125, device="cuda") if bias else None
+    logits = c.logits(E + T, 1.0)
+    n = E // G
+    l = logits.double().cpu()
+    worth = log_scores(c, l).exp().view(T, G, n).sort(dim=2, descending=True).values[..., :2].sum(2)
+    order = torch.argsort(-worth, dim=1, stable=True)
+    rows = range(0, T, 5)
+    for i, t in enumerate(list(rows)[:40]):
+        a, b = int(order[t, Kg - 1]), int(order[t, Kg])
+        v = logits[t, a * n:(a + 1) * n].flip(0)
+        if i % 3:
+            v[v.argmax()] *= 1 + (2.0 ** -23 if i % 3 == 1 else -2.0 ** -23)
+        logits[t, b * n:(b + 1) * n] = v
+    check(c, logits, flat)
+    if T > 3:
+        logits[3, E - 1] = float("nan")
+        idx, w = c.run(logits, flat)
+        assert moe.moe_poll_status(c.ws) != 0
+        want = choose(c, torch.nan_to_num(logits), flat)
+        keep = torch.arange(T) != 3
+        assert torch.equal(idx.cpu().long()[keep], want[keep])
+        assert bool(torch.isnan(w[3]).all()) and torch.equal(idx[3].cpu(), torch.arange(k, dtype=torch.int32))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias", [False, True])
 def test_equal_candidates_go_to_the_lowest_index(score, bias):
