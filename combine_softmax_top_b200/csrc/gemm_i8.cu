@@ -539,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
             ptx::named_barrier(2 + set, 128);
             if (first + h < j.rows) {
               const int* other = gate ? xu : xg;
+              float g[8], u[8];
 #pragma unroll
               for (int c = 0; c < 8; c += 4) {
                 const float4 s4 = *reinterpret_cast<const float4*>(xs + first + h + c);
@@ -546,10 +547,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const int own = (int)(gate ? v[h + c + i] : v[16 + h + c + i]), far = other[(c + i) * 64 + ch];
-                  const float g = (float)(gate ? own : far) * sw * s[i], u = (float)(gate ? far : own) * su * s[i];
-                  f[h + c + i] = i8::swiglu<O>(g, u);
+                  g[c + i] = (float)(gate ? own : far) * sw * s[i];
+                  u[c + i] = (float)(gate ? far : own) * su * s[i];
                 }
               }
+              i8::swiglu<O>(g, u, f + h);
             }
             ptx::named_barrier(2 + set, 128);
           }

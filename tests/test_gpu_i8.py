@@ -524,3 +524,21 @@ def test_int8_layer_of_the_stages(T, compact):
     (gr,) = torch.autograd.grad((2.0 * sel / sel.sum(1, keepdim=True) * gw.double().cpu()).sum(), l)
     bound = 2 * (4 * 6 + 96) * U * 2 * 2 * gw.double().cpu().abs().sum(1, keepdim=True)
     assert bool(((gl.double().cpu() - gr).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(1, 300, 16), (8, 2400, 32), (40, 200, 144), (64, 130, 8192), (300, 520, 272),
+                                   (1200, 1040, 160)])
+def test_swiglu_of_gates_far_below_zero(M, N, K, out, ws):
+    """Gates of -127 .. 20, exact, against ups large enough that silu(g) u is a
+    normal number where exp(-g) is beyond binary32."""
+    x, w, wu = (torch.zeros(s, dtype=torch.int8) for s in ((M, K), (N, K), (N, K)))
+    x[:, 3] = 1
+    w[:, 3] = (torch.arange(N) % 148 - 127).to(torch.int8)
+    wu[:, 3] = (torch.arange(N) % 251 - 125).to(torch.int8)
+    one, us = torch.ones(max(M, N)), torch.full((N,), 2.0 ** 60)
+    y = torch.empty(M, N, dtype=DT[out], device="cuda")
+    dev = [t.cuda() for t in (x, one[:M], w, one[:N], wu, us)]
+    moe.moe_gemm_i8(*dev[:4], y, ws, w_up=dev[4], up_scale=dev[5])
+    assert moe.moe_poll_status(ws) == 0
+    close(y, *gemm_ref(x, one[:M], w, one[:N], wu, us), out, True)
