@@ -150,6 +150,16 @@ __device__ __forceinline__ bool sub_any(bool p) {
   return ((all >> ((threadIdx.x & 31) / S * S)) & ((1u << (S & 31)) - 1u)) != 0u;
 }
 
+// exp(x), x <= 0, for a gradient of type T: binary32's own for binary32. What is
+// rounded to bf16 takes the quick one, off by (4 + 1.5 |x|) 2^-24 relative (see
+// quick_exp): 2^-17 for the smallest normal result, half a step of bf16 is 2^-8.
+// For binary32 that would be up to 134 half-units where expf has 4; it costs 8192 x
+// 256 4.3 -> 4.8 us, and nothing where HBM bounds (32768 x 1024 42 us).
+template <typename T>
+__device__ __forceinline__ float grad_exp(float x) {
+  return sizeof(T) == 2 ? __expf(x) : expf(x);
+}
+
 constexpr float kLog2E = 1.4426950408889634f;
 __device__ __forceinline__ float quick_exp2(float x) {
   float r;
@@ -719,7 +729,7 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
     float z = 0.f;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      p[c] = p[c] == -INFINITY ? 0.f : __expf(p[c] - top);
+      p[c] = p[c] == -INFINITY ? 0.f : grad_exp<T>(p[c] - top);
       z += p[c];
     }
     inv = 1.f / sub_sum<S>(z);
@@ -734,14 +744,14 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
 #pragma unroll
       for (int b = 1; b < kW; ++b) vm = fmaxf(vm, v[b]);
       if (vm > m) {
-        z *= __expf(m - vm);
+        z *= grad_exp<T>(m - vm);
         m = vm;
       }
 #pragma unroll
-      for (int b = 0; b < kW; ++b) z += v[b] == -INFINITY ? 0.f : __expf(v[b] - m);
+      for (int b = 0; b < kW; ++b) z += v[b] == -INFINITY ? 0.f : grad_exp<T>(v[b] - m);
     }
     top = sub_max<S>(m);
-    z = sub_sum<S>(z == 0.f ? 0.f : z * __expf(m - top));
+    z = sub_sum<S>(z == 0.f ? 0.f : z * grad_exp<T>(m - top));
     inv = 1.f / z;
     dot = sub_sum<S>(live ? gw * (expf(l - top) * inv) : 0.f);
   }
@@ -760,7 +770,7 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
       if constexpr (kEvery) {
         load_vec<kW>(row + i, v);
 #pragma unroll
-        for (int b = 0; b < kW; ++b) v[b] = __expf(v[b] - top) * inv * -dot;
+        for (int b = 0; b < kW; ++b) v[b] = grad_exp<T>(v[b] - top) * inv * -dot;
       } else {
 #pragma unroll
         for (int b = 0; b < kW; ++b) v[b] = 0.f;

@@ -425,3 +425,25 @@ def test_gate_agrees_with_route_where_both_apply():
     torch.cuda.synchronize()
     assert torch.equal(idx, ri)
     assert torch.allclose(w, rw, rtol=2 * tol(logits), atol=0)
+
+
+@pytest.mark.parametrize("E", [64, 256, 516, 1024, 66, 1001])
+def test_softmax_gradient_of_far_experts_is_binary32s(E):
+    """Logits 20 to 84 below the only chosen one, in steps that subtract exactly,
+    so that the probability is one exp, off by 2 * 2^-23 = 4 U (U = 2^-24), times
+    1 / z. z is 1 but for the others (1024 / 64 e^-20 / (1 - e^-(1/16)) < 0.6 U),
+    one rounding as they are added, one of the reciprocal: 2.6 U, in p_e and in
+    the sum over the chosen. With three products: 4 + 5.2 + 3 < 13 U."""
+    c = Case(70, E=E, k=1, renorm=0)
+    far = -(20 + 64 * torch.arange(E, dtype=torch.float64) / E)
+    l = (far * 1024).round() / 1024
+    l = l.repeat(70, 1)
+    idx = torch.arange(70)[:, None] * 7 % E
+    l.scatter_(1, idx, 0.0)
+    l += torch.arange(70)[:, None].double() % 5          # every logit a multiple of 2^-10 below 2^7
+    got = c.back(l.float().cuda(), idx.int().cuda(), torch.full((70, 1), 3.0, device="cuda")).double().cpu()
+    p = torch.softmax(l, 1)
+    want = 3 * p.gather(1, idx) * -p
+    other = torch.ones_like(l, dtype=torch.bool).scatter_(1, idx, False)
+    off = ((got - want).abs() / want.abs())[other]
+    assert float(off.max()) <= 13 * U, float(off.max()) / U
