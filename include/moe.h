@@ -476,7 +476,16 @@ MOE_API moe_status moe_gate(const moe_shape* shape, const moe_gate_desc* gate, c
  *   grad_w      [T, topk] fp32, device
  *   grad_logits [T, E] gate->logits_dtype, device (out, every element written)
  * With a shared expert topk_idx and grad_w have topk + 1 columns, the last
- * without effect. The order of sums is fixed. Non-finite logits give NaN.
+ * without effect. The order of sums is fixed.
+ * Nothing is latched for logits that are not finite. Only those the formula needs
+ * are read: the whole row for a plain softmax (renorm 0), else those of the chosen
+ * experts; an expert whose logit is not read gets 0.
+ *   NaN         makes all that depends on it NaN: the row of a plain softmax, the
+ *               chosen experts of renormalised scores, of a plain sigmoid the
+ *               expert itself
+ *   -infinity   a score of 0, with gradient 0; where a softmax or renormalised
+ *               scores have nothing else, NaN
+ *   +infinity   like NaN in a softmax; for a sigmoid a score of 1, with gradient 0
  */
 MOE_API moe_status moe_gate_backward(const moe_shape* shape, const moe_gate_desc* gate, const void* logits,
                                      const int32_t* topk_idx, const float* grad_w, void* grad_logits,

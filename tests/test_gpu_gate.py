@@ -447,3 +447,57 @@ def test_softmax_gradient_of_far_experts_is_binary32s(E):
     other = torch.ones_like(l, dtype=torch.bool).scatter_(1, idx, False)
     off = ((got - want).abs() / want.abs())[other]
     assert float(off.max()) <= 13 * U, float(off.max()) / U
+
+
+def _gradient_by_case(c, l, idx, g):
+    """(gradient, what its differences are made of) of finite and other logits, 64
+    bits: an infinity counts as its limit where there is one."""
+    s = torch.sigmoid(l).gather(1, idx)
+    if c.score == "softmax":
+        p = torch.softmax(l if not c.renorm else l.gather(1, idx), 1)      # +inf and NaN: a row of NaN
+        q = p if c.renorm else p.gather(1, idx)
+    else:
+        # s / sum s by a factor common to all, so that no share underflows
+        ls = -torch.logaddexp(torch.zeros_like(l), -l).gather(1, idx)
+        q = torch.softmax(ls, 1) if c.renorm else s
+    part, size = (q * g).sum(1, keepdim=True), (q * g).abs().sum(1, keepdim=True)
+    grad, made = torch.zeros_like(l), torch.zeros_like(l)
+    if c.score == "softmax" and not c.renorm:
+        grad, made = -p * part, p * size
+    rest = 1 - s if c.score == "sigmoid" else torch.ones_like(s)           # of +inf 0, of -inf 1
+    d = q * (g - part) if c.renorm else q * g
+    grad.scatter_add_(1, idx, c.scale * d * rest)
+    # a plain sigmoid's gradient of one expert is made of nothing of the others
+    alone = c.score == "sigmoid" and not c.renorm
+    made.scatter_add_(1, idx, abs(c.scale) * q * (g.abs() if alone else g.abs() + size))
+    return grad, made
+
+
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16])
+@pytest.mark.parametrize("score,renorm", [("softmax", 0), ("softmax", 1), ("sigmoid", 0), ("sigmoid", 1)])
+@pytest.mark.parametrize("E,k", [(128, 6), (256, 8), (512, 9), (1000, 6), (63, 5), (1002, 12)])
+def test_gradient_of_logits_that_are_not_finite(E, k, score, renorm, dtype):
+    """NaN and the infinities at chosen experts and at others: what depends on
+    them as include/moe.h says, and nothing else."""
+    values = [float("nan"), float("inf"), float("-inf")]
+    c = Case(40, E=E, k=k, score=score, renorm=renorm, dtype=dtype)
+    logits = c.logits(3)
+    idx = torch.stack([torch.randperm(E, generator=torch.Generator().manual_seed(t))[:k] for t in range(40)])
+    for t in range(36):                       # rows 36 .. 39 stay finite
+        row = idx[t].tolist()
+        other = next(e for e in range(E) if e not in row)
+        at = [row[0], other, row[k - 1]][t % 3]
+        logits[t, at] = values[t // 3 % 3]
+        if t >= 18:                           # two values in a row, one chosen and one not
+            logits[t, row[1]] = values[t // 9 % 3]
+            logits[t, E - 1 if E - 1 not in row else other] = values[t // 2 % 3]
+        if t >= 33:                           # every chosen expert
+            logits[t, idx[t]] = values[t % 3]
+    gw = torch.randn(40, k, generator=torch.Generator().manual_seed(5)).cuda()
+    got = c.back(logits, idx.int().cuda(), gw).double().cpu()
+    want, made = _gradient_by_case(c, logits.double().cpu(), idx, gw.double().cpu())
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    ok = ~torch.isnan(want)
+    finite = logits.double().cpu()
+    bound = 2 * tol(finite[torch.isfinite(finite)]) * made + (2.0 ** -8 * want.abs() if dtype == W.BF16 else 0) + 2.0 ** -126
+    assert bool(((got - want).abs() <= bound)[ok].all())
