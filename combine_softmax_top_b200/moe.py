@@ -316,6 +316,18 @@ def _dense(fn: str, name: str, t, shape, dtypes, dev: int) -> int:
     return t.data_ptr()
 
 
+_HEADER_BYTES = 256   # of a workspace: where the library latches errors
+
+
+def _workspace(fn: str, ws, dev: int) -> int:
+    """Address of a workspace's memory on device `dev`, at least its header."""
+    if ws is None or ws.get_device() != dev or not ws.is_contiguous() or ws.nbytes < _HEADER_BYTES:
+        got = "None" if ws is None else f"{ws.nbytes} bytes, strides {ws.stride()} on {ws.device}"
+        raise ValueError(f"{fn}: ws must be a contiguous workspace on the current CUDA device, prepared by "
+                         f"moe_workspace_init, got {got}")
+    return ws.data_ptr()
+
+
 _F32, _I32, _I8 = (torch.float32,), (torch.int32,), (torch.int8,)
 _FLOATS = (torch.float32, torch.bfloat16)
 _SRC = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
@@ -335,7 +347,7 @@ def moe_gate(shape, gate: moe_gate_desc, logits, bias, topk_idx, topk_w, ws, str
     dev, st = _begin(fn, "logits", logits, stream)
     pl, pi, pw = _gate_args(fn, shape, gate, logits, topk_idx, topk_w, dev)
     pb = None if bias is None else _dense(fn, "bias", bias, (shape.E,), _F32, dev)
-    _check(fn, lib().moe_gate(ctypes.byref(shape), ctypes.byref(gate), pl, pb, pi, pw, ws.data_ptr(), st))
+    _check(fn, lib().moe_gate(ctypes.byref(shape), ctypes.byref(gate), pl, pb, pi, pw, _workspace(fn, ws, dev), st))
 
 
 def moe_gate_backward(shape, gate: moe_gate_desc, logits, topk_idx, grad_w, grad_logits, stream=None) -> None:
@@ -396,7 +408,8 @@ def moe_gemm_i8(x, x_scale, w, w_scale, y, ws, w_up=None, up_scale=None, offsets
         pus = _dense(fn, "up_scale", up_scale, wshape[:-1], _F32, dev)
     py = _dense(fn, "y", y, (M, N), _FLOATS, dev)
     d = moe_gemm_i8_desc(M, N, K, E, fill, _SRC[y.dtype], 0)
-    _check(fn, lib().moe_gemm_i8(ctypes.byref(d), px, pxs, pw, pws, pu, pus, po, pc, py, ws.data_ptr(), st))
+    _check(fn, lib().moe_gemm_i8(ctypes.byref(d), px, pxs, pw, pws, pu, pus, po, pc, py,
+                                 _workspace(fn, ws, dev), st))
 
 
 def moe_dispatch_noalloc(shape, x, topk_idx, bufs: moe_dispatch_bufs, stream=None) -> None:

@@ -127,3 +127,48 @@ def test_python_binding_refuses_what_the_library_cannot_see():
         moe.moe_gate(_shape(), _gate(), torch.zeros(4, 64), None, None, None, None)
     with pytest.raises(KeyError):
         moe.make_gate("softmin")
+
+
+class _FakeLibrary:
+    """Takes every call and notes the workspace's address."""
+
+    def __init__(self):
+        self.seen = []
+
+    def moe_gate(self, *args):
+        self.seen.append(args[-2])
+        return OK
+
+    moe_gemm_i8 = moe_gate
+
+
+@pytest.mark.parametrize("call", ["moe_gate", "moe_gemm_i8"])
+def test_python_binding_refuses_workspaces_it_cannot_write_to(call, monkeypatch):
+    """The library latches errors into a workspace's first 256 bytes: host memory, a
+    shorter tensor or a strided one never get that far. Host tensors stand for
+    the current device's here (device -1), and a fake for the library."""
+    fake = _FakeLibrary()
+    monkeypatch.setattr(moe, "lib", lambda: fake)
+    monkeypatch.setattr(moe, "_begin", lambda fn, name, t, stream: (-1, 0))
+
+    def run(ws):
+        if call == "moe_gate":
+            moe.moe_gate(_shape(), _gate(), torch.zeros(4, 64), None, torch.zeros(4, 4, dtype=torch.int32),
+                         torch.zeros(4, 4), ws)
+        else:
+            moe.moe_gemm_i8(torch.zeros(4, 128, dtype=torch.int8), torch.zeros(4), torch.zeros(8, 128, dtype=torch.int8),
+                            torch.zeros(8), torch.zeros(4, 8), ws)
+
+    good = torch.zeros(256, dtype=torch.uint8)
+    run(good)
+    run(torch.zeros(64, dtype=torch.int32))
+    assert fake.seen[0] == good.data_ptr() and len(fake.seen) == 2
+    for bad in (None, torch.zeros(255, dtype=torch.uint8), torch.zeros(0, dtype=torch.uint8),
+                torch.zeros(1024, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match=f"{call}: ws must be"):
+            run(bad)
+    monkeypatch.setattr(moe, "_dense", lambda fn, name, t, shape, dtypes, dev: t.data_ptr())
+    monkeypatch.setattr(moe, "_begin", lambda fn, name, t, stream: (0, 0))   # device 0 is current, ws is the host's
+    with pytest.raises(ValueError, match=f"{call}: ws must be"):
+        run(good)
+    assert len(fake.seen) == 2
