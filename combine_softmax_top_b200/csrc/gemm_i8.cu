@@ -584,11 +584,17 @@ template <int kForm, bool kUp, typename O>
 cudaError_t launch(const GemmI8Args& a, int team, bool wide) {
   using F = Form<kForm, kUp>;
   constexpr int kMaxDevices = 64;
-  static std::atomic<int> resident[kMaxDevices][3];   // clusters of 1, 2, 4 at once on each device, 0 = not asked yet
+  static std::atomic<bool> prepared[kMaxDevices];   // the kernel's shared memory is allowed on this device
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!prepared[dev].load(std::memory_order_acquire)) {
+    if ((err = cudaFuncSetAttribute(gemm_i8_kernel<kForm, kUp, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    F::kSmem)) != cudaSuccess)
+      return err;
+    prepared[dev].store(true, std::memory_order_release);
+  }
 
   Params p;
   memset(&p, 0, sizeof(p));
@@ -624,19 +630,16 @@ cudaError_t launch(const GemmI8Args& a, int team, bool wide) {
   cfg.stream = a.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  std::atomic<int>& known = resident[dev][team == 1 ? 0 : team == 2 ? 1 : 2];
-  int workers = known.load(std::memory_order_acquire);
-  if (workers == 0) {
-    if ((err = cudaFuncSetAttribute(gemm_i8_kernel<kForm, kUp, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    F::kSmem)) != cudaSuccess)
-      return err;
+  // no more workers than the most units there can be, and where that does not
+  // settle it, no more than are resident at once: of the SMs of this stream (a green
+  // context may have few), so it is asked each time
+  const int64_t most = (ceil_div(a.d.M, F::kFull) + (a.win.offsets ? E : 0)) * p.tiles;
+  int workers = fit;
+  if (most > fit) {
     if (cudaOccupancyMaxActiveClusters(&workers, gemm_i8_kernel<kForm, kUp, O>, &cfg) != cudaSuccess || workers < 1)
       workers = fit;
     (void)cudaGetLastError();   // a failed query is not the launch's error
-    known.store(workers, std::memory_order_release);
   }
-  // no more workers than the most units there can be
-  const int64_t most = (ceil_div(a.d.M, F::kFull) + (a.win.offsets ? E : 0)) * p.tiles;
   cfg.gridDim.x = (unsigned)(team * std::min<int64_t>(std::min(workers, fit), most));
   return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<kForm, kUp, O>, p);
 }

@@ -542,3 +542,44 @@ def test_swiglu_of_gates_far_below_zero(M, N, K, out, ws):
     moe.moe_gemm_i8(*dev[:4], y, ws, w_up=dev[4], up_scale=dev[5])
     assert moe.moe_poll_status(ws) == 0
     close(y, *gemm_ref(x, one[:M], w, one[:N], wu, us), out, True)
+
+
+def test_first_call_on_few_sms_leaves_later_ones_the_device():
+    """A process whose first product runs on a green context of a few SMs: the
+    next ones, on the whole device, are spread over all of it (an eighth of the
+    SMs at most against all: 8 times the rate; 3 times is asked for)."""
+    code = """
+import torch
+from combine_softmax_top_b200 import moe, workloads as W
+sh = moe.make_shape(W.spec("tiny"))
+ws = torch.empty(moe.moe_workspace_bytes(sh), dtype=torch.uint8, device="cuda")
+moe.moe_workspace_init(sh, ws)
+x, xs = torch.ones(4096, 4096, dtype=torch.int8, device="cuda"), torch.ones(4096, device="cuda")
+w, wsc = torch.ones(4096, 4096, dtype=torch.int8, device="cuda"), torch.ones(4096, device="cuda")
+y = torch.empty(4096, 4096, dtype=torch.bfloat16, device="cuda")
+x1, w1, y1 = x[:128], w[:, :512].contiguous(), torch.empty(128, 4096, dtype=torch.bfloat16, device="cuda")
+x1 = x1[:, :512].contiguous()
+part = moe.GreenPartition(16, 0)
+assert part.dispatch_sms * 8 <= part.dispatch_sms + part.main_sms
+few = torch.cuda.ExternalStream(part.dispatch_stream)
+forms = [lambda s: moe.moe_gemm_i8(x, xs, w, wsc, y, ws, stream=s),                  # a CTA pair a unit
+         lambda s: moe.moe_gemm_i8(x1, xs[:128], w1, wsc, y1, ws, stream=s)]         # one CTA a unit
+
+def us(f, s, n):
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    best = 1e30
+    for _ in range(n):
+        a.record(s); f(s); b.record(s); b.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+torch.cuda.synchronize()
+times = [(us(f, few, 3), us(f, torch.cuda.current_stream(), 5)) for f in forms]
+assert moe.moe_poll_status(ws) == 0
+part.close()
+print("times", times)
+assert times[0][1] * 3 < times[0][0], times
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr[-2000:]
