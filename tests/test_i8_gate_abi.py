@@ -172,3 +172,19 @@ def test_python_binding_refuses_workspaces_it_cannot_write_to(call, monkeypatch)
     with pytest.raises(ValueError, match=f"{call}: ws must be"):
         run(good)
     assert len(fake.seen) == 2
+
+
+@pytest.mark.parametrize("over", [
+    # units (chunks of 64 rows, one more an expert, times tiles of 64 channels) that
+    # 32 bits do not count: by the channels, and by the experts alone
+    dict(M=(1 << 31) - 512, N=4097, K=16),
+    dict(M=(1 << 31) - 512, N=4096, K=16, experts=9, off=P, cnt=P),
+])
+def test_gemm_refuses_more_units_than_32_bits(over):
+    assert _gemm(**over) == INVALID
+
+
+def test_gate_refuses_more_than_32_groups():
+    """Where nothing else about 64 groups of one expert is wrong."""
+    g = _gate(groups=64, topk_groups=64, group_best=1)
+    assert _call_gate(_shape(), g) == INVALID and _call_back(_shape(), g) == INVALID
