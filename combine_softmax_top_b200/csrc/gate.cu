@@ -686,14 +686,15 @@ again:
 }
 
 // S lanes a token (topk <= S). Elements go kW at a time, 16 bytes where rows
-// start on such a boundary, else one. With NV > 0 a plain softmax keeps its row in
-// NV registers a lane (E <= S NV): one exponential an element instead of two.
+// start on such a boundary, else one. In the former case a plain softmax keeps its
+// row in NV > 0 registers a lane (E <= S NV): one exponential an element, not two.
 template <typename T, bool kSigmoid, bool kRenorm, int S, int kW, int NV>
 __global__ void __launch_bounds__(kWarps * 32)
 gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ topk_idx,
                      const float* __restrict__ grad_w, int tokens, int E, int k, int shared, float scale,
                      T* __restrict__ grad_logits) {
   constexpr bool kEvery = !kSigmoid && !kRenorm;
+  static_assert(!kEvery || (NV > 0) == (kW > 1), "a plain softmax's row is in registers where it is loaded wide");
   const int lane = threadIdx.x & 31, li = lane % S, base = lane - li;
   const int warp_t = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * (32 / S);
   if (warp_t >= tokens) return;
@@ -735,20 +736,15 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
     inv = 1.f / sub_sum<S>(z);
     dot = sub_sum<S>(live ? gw * (expf(l - top) * inv) : 0.f);
   } else if constexpr (kEvery) {
-    // running maximum and sum in one pass
+    // running maximum and sum in one pass, an element at a time (E is of no wide load)
     float m = -INFINITY, z = 0.f;
-    for (int i = li * kW; i < E; i += S * kW) {
-      float v[kW];
-      load_vec<kW>(row + i, v);
-      float vm = v[0];
-#pragma unroll
-      for (int b = 1; b < kW; ++b) vm = fmaxf(vm, v[b]);
-      if (vm > m) {
-        z *= grad_exp<T>(m - vm);
-        m = vm;
+    for (int i = li; i < E; i += S) {
+      const float v = load_logit(row + i);
+      if (v > m) {
+        z *= grad_exp<T>(m - v);
+        m = v;
       }
-#pragma unroll
-      for (int b = 0; b < kW; ++b) z += v[b] == -INFINITY ? 0.f : grad_exp<T>(v[b] - m);
+      z += v == -INFINITY ? 0.f : grad_exp<T>(v - m);
     }
     top = sub_max<S>(m);
     z = sub_sum<S>(z == 0.f ? 0.f : z * grad_exp<T>(m - top));
@@ -756,27 +752,20 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
     dot = sub_sum<S>(live ? gw * (expf(l - top) * inv) : 0.f);
   }
   // what every expert gets
-  if (kEvery && NV > 0) {
+  if constexpr (kEvery && NV > 0) {
 #pragma unroll
     for (int c = 0; c < NV; c += kW) {
       float v[kW];
 #pragma unroll
-      for (int b = 0; b < kW; ++b) v[b] = p[kEvery && NV > 0 ? c + b : 0] * inv * -dot;
+      for (int b = 0; b < kW; ++b) v[b] = p[c + b] * inv * -dot;
       if (real && li * kW + c * S < E) store_vec<kW>(grow + li * kW + c * S, v);
     }
+  } else if constexpr (kEvery) {
+    if (real)
+      for (int i = li; i < E; i += S) store_grad(grow + i, grad_exp<T>(load_logit(row + i) - top) * inv * -dot);
   } else if (real) {
-    for (int i = li * kW; i < E; i += S * kW) {
-      float v[kW];
-      if constexpr (kEvery) {
-        load_vec<kW>(row + i, v);
-#pragma unroll
-        for (int b = 0; b < kW; ++b) v[b] = grad_exp<T>(v[b] - top) * inv * -dot;
-      } else {
-#pragma unroll
-        for (int b = 0; b < kW; ++b) v[b] = 0.f;
-      }
-      store_vec<kW>(grow + i, v);
-    }
+    const float none[kW] = {};
+    for (int i = li * kW; i < E; i += S * kW) store_vec<kW>(grow + i, none);
   }
   // and what the chosen ones get: d from slot li
   float d;
@@ -876,12 +865,12 @@ cudaError_t launch_gate_backward(const moe_shape& s, const moe_gate_desc& g, con
       if (E % kV == 0 && k <= 8 && E <= 256) return go(gate_backward_kernel<L, kSig, kRen, 8, kV, 32>, l, d, 8);
       if (E % kV == 0 && E <= 512) return go(gate_backward_kernel<L, kSig, kRen, 32, kV, 16>, l, d, 32);
       if (E % kV == 0) return go(gate_backward_kernel<L, kSig, kRen, 32, kV, 32>, l, d, 32);
+    } else {
+      if (E % kV == 0 && k <= 8) return go(gate_backward_kernel<L, kSig, kRen, 8, kV, 0>, l, d, 8);
+      if (E % kV == 0) return go(gate_backward_kernel<L, kSig, kRen, 32, kV, 0>, l, d, 32);
     }
-    if (k <= 8)
-      return E % kV == 0 ? go(gate_backward_kernel<L, kSig, kRen, 8, kV, 0>, l, d, 8)
-                         : go(gate_backward_kernel<L, kSig, kRen, 8, 1, 0>, l, d, 8);
-    return E % kV == 0 ? go(gate_backward_kernel<L, kSig, kRen, 32, kV, 0>, l, d, 32)
-                       : go(gate_backward_kernel<L, kSig, kRen, 32, 1, 0>, l, d, 32);
+    return k <= 8 ? go(gate_backward_kernel<L, kSig, kRen, 8, 1, 0>, l, d, 8)
+                  : go(gate_backward_kernel<L, kSig, kRen, 32, 1, 0>, l, d, 32);
   };
   auto by_form = [&](auto* l, auto* d) {
     std::true_type yes;

@@ -474,7 +474,8 @@ MOE_API moe_status moe_gate(const moe_shape* shape, const moe_gate_desc* gate, c
  *               [0, E) takes no part, as if it had not been chosen; an expert
  *               named twice counts twice (in the sum of renormalised weights too)
  *   grad_w      [T, topk] fp32, device
- *   grad_logits [T, E] gate->logits_dtype, device (out, every element written)
+ *   grad_logits [T, E] gate->logits_dtype, device (out, every element written); it
+ *               must not overlap the inputs
  * With a shared expert topk_idx and grad_w have topk + 1 columns, the last
  * without effect. The order of sums is fixed.
  * Nothing is latched for logits that are not finite. Only those the formula needs
