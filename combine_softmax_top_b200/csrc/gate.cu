@@ -736,15 +736,24 @@ gate_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ t
     inv = 1.f / sub_sum<S>(z);
     dot = sub_sum<S>(live ? gw * (expf(l - top) * inv) : 0.f);
   } else if constexpr (kEvery) {
-    // running maximum and sum in one pass, an element at a time (E is of no wide load)
+    // running maximum and sum in one pass, an element a load (E is of no wide one).
+    // expf's elements wait for one rescaling together (1002 f32, one token / 32768:
+    // 11 / 95 us, each by itself 17 / 103); quick ones do not gain (bf16 67, 64 us)
+    constexpr int kEach = sizeof(T) == 4 ? 16 : 1;
     float m = -INFINITY, z = 0.f;
-    for (int i = li; i < E; i += S) {
-      const float v = load_logit(row + i);
-      if (v > m) {
-        z *= grad_exp<T>(m - v);
-        m = v;
+    for (int i = li; i < E; i += kEach * S) {
+      float v[kEach];
+#pragma unroll
+      for (int b = 0; b < kEach; ++b) v[b] = i + b * S < E ? load_logit(row + i + b * S) : -INFINITY;
+      float vm = v[0];
+#pragma unroll
+      for (int b = 1; b < kEach; ++b) vm = fmaxf(vm, v[b]);
+      if (vm > m) {
+        z *= grad_exp<T>(m - vm);
+        m = vm;
       }
-      z += v == -INFINITY ? 0.f : grad_exp<T>(v - m);
+#pragma unroll
+      for (int b = 0; b < kEach; ++b) z += v[b] == -INFINITY ? 0.f : grad_exp<T>(v[b] - m);
     }
     top = sub_max<S>(m);
     z = sub_sum<S>(z == 0.f ? 0.f : z * grad_exp<T>(m - top));
