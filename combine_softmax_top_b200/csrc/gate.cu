@@ -831,14 +831,26 @@ cudaError_t launch_gate(const Ctx& c, const moe_gate_desc& g, const void* logits
     constexpr bool kSig = decltype(sig)::value, kClose = decltype(close)::value;
     // a lane for every slot and, where the keys are not exact, the best one left
     const int lanes = std::max(k + (sizeof(L) == 2 && !bias ? 0 : 1), (int)g.groups);
-    // Fewer lanes a token once the SMs are full of warps anyway. Measured, warp
-    // against part: 6000 x 128 bf16 4.1 / 3.6 us, 4096 3.2 / 3.2, 2048 2.6 / 2.9;
-    // 8192 x 64 f32 5.4 / 4.9, 4096 3.8 / 4.2; 16384 x 160 bf16 with groups 12.3 /
-    // 11.4, 8192 7.2 / 6.9
-    if (T >= 4096 && lanes <= 8 && E <= 128)
+    // Fewer lanes a token once the SMs are full of warps anyway; later where the
+    // choice needs scores, as a token in doubt keeps the others of its warp waiting,
+    // longest for a softmax's sum. Measured, a warp / 8 lanes: 128 bf16, 4096 tokens
+    // 3.2 / 3.1 us, 2048 2.6 / 2.9; 64 f32, 4096 3.9 / 2.9, 2048 3.2 / 3.3. With scores,
+    // sigmoid: 64 f32, 4096 4.3 / 4.0; 128 f32, 8192 6.2 / 5.9, 4096 4.4 / 4.8; softmax:
+    // 64 f32, 6000 5.4 / 5.1, 4096 4.3 / 5.0; 96 f32, 10240 7.9 / 8.0, 6000 5.8 / 7.0.
+    // 16 lanes: 128 f32, 8192 5.5 / 5.0, 4096 4.2 / 4.4; sigmoid with a bias 8192 6.3 /
+    // 5.7, and groups 12288 9.7 / 8.6, 8192 7.5 / 9.0.
+    // Beyond 128 experts it is a matter of little: 16384 x 256 bf16 9.0 / 8.7, 12288
+    // 7.3 / 7.3; 16384 x 160 bf16 with groups 12.3 / 11.5, 12288 9.7 / 9.4; with scores
+    // 160 f32 and groups 16384 14.3 / 13.1, 12288 13.0 / 14.2; 256 never (32768, f32 and
+    // groups 25.4 / 28.0)
+    const bool scores = bias || (g.groups > 1 && g.group_best == 2);
+    const int from8 = !scores ? 4096 : E <= 64 ? (kSig ? 4096 : 6000) : (kSig ? 8192 : 10240);
+    if (lanes <= 8 && E <= 128 && T >= from8)
       return E <= 64 ? go(gate_kernel<L, kSig, 8, 8, false>, l, 8, 8) : go(gate_kernel<L, kSig, 16, 8, false>, l, 8, 16);
-    if (T >= (E <= 128 ? 8192 : 12288) && lanes <= 16 && E <= 256)
-      return E <= 128 ? go(gate_kernel<L, kSig, 8, 16, false>, l, 16, 8) : go(gate_kernel<L, kSig, 16, 16, false>, l, 16, 16);
+    if (lanes <= 16 && E <= 128 && T >= (scores && (!kSig || g.groups > 1) ? 10240 : 8192))
+      return go(gate_kernel<L, kSig, 8, 16, false>, l, 16, 8);
+    if (lanes <= 16 && E <= (scores ? 192 : 256) && T >= (scores ? 16384 : 12288))
+      return go(gate_kernel<L, kSig, 16, 16, false>, l, 16, 16);
     if (E <= 128) return go(gate_kernel<L, kSig, 4, 32, kClose>, l, 32, 4);
     if (E <= 256) return go(gate_kernel<L, kSig, 8, 32, kClose>, l, 32, 8);
     if (E <= 512) return go(gate_kernel<L, kSig, 16, 32, kClose>, l, 32, 16);

@@ -501,3 +501,16 @@ def test_gradient_of_logits_that_are_not_finite(E, k, score, renorm, dtype):
     finite = logits.double().cpu()
     bound = 2 * tol(finite[torch.isfinite(finite)]) * made + (2.0 ** -8 * want.abs() if dtype == W.BF16 else 0) + 2.0 ** -126
     assert bool(((got - want).abs() <= bound)[ok].all())
+
+
+@pytest.mark.parametrize("T", [4095, 4096, 5999, 6000, 8191, 10239, 10240, 12288, 16383, 16385])
+@pytest.mark.parametrize("form", [
+    dict(E=64, k=7, renorm=0), dict(E=60, k=6, score="sigmoid", bias=True), dict(E=64, k=6, groups=8, topk_groups=4, best=2),
+    dict(E=128, k=8, dtype=W.BF16), dict(E=100, k=6, bias=True, dtype=W.BF16), dict(E=128, k=12, bias=True, score="sigmoid"),
+    dict(E=160, k=6, score="sigmoid", bias=True, groups=8, topk_groups=3, best=2), dict(E=250, k=15, dtype=W.BF16),
+    dict(E=192, k=8, bias=True, renorm=0), dict(E=196, k=8, bias=True),
+], ids=lambda f: "-".join(f"{k}{v}" for k, v in f.items()))
+def test_gate_around_the_sizes_where_lanes_change(form, T):
+    """Fewer lanes take a token from some of these sizes on."""
+    c = Case(T, **form)
+    check(c, c.logits(T), c.make_bias())
