@@ -22,16 +22,18 @@
 // c is the logit itself; bf16 logits then lose nothing in the keys and need no
 // second look.
 //
-// Bound by instruction issue for many tokens (709 warp instructions a token of
-// 256 f32 logits with a bias and groups, 143 of 128 bf16 ones), by latency for
-// few: one token 2.7 us, 8192 x 256 f32 8.7 us, 32768 x 128 bf16 8.1 us
-// (1.0 and 1.0 TB/s of logits, where HBM would allow 6.5).
+// For many tokens neither HBM nor issue is the bound, but rounds of warps, each
+// with its load uncovered: 709 warp instructions a token of 256 f32 logits with a
+// bias and groups take 69 % of the issue slots (40 registers: 48 warps an SM for
+// 55 tokens an SM of 8192), 143 of 128 bf16 ones 52 % (69 to 72 registers: 28 warps
+// an SM for 55). For few it is latency. One token 2.7 us, 8192 x 256 f32 8.8 us, 32768
+// x 128 bf16 8.2 us (1.0 and 1.0 TB/s of logits, where HBM would allow 6.5).
 //
 // gate_backward_kernel writes what every expert gets (zero, or -p_e dot for a
 // plain softmax) 16 bytes a lane, then the chosen experts' derivatives over it.
 // The row is read only for a plain softmax, once where registers hold it. 8192 x
-// 256 f32, renormalised: 3.5 us (2.6 TB/s); 32768 x 128 bf16, plain softmax, 5.2 us
-// (3.6 TB/s).
+// 256 f32, renormalised: 3.4 us (2.7 TB/s); 32768 x 128 bf16, plain softmax, 4.9 us
+// (3.9 TB/s), both mostly launch and latency; 32768 x 1024 f32 42 us (6.4 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -439,7 +441,8 @@ again:
   // 2^-24, the reciprocal 2^-23: 4.6 * 2^-24. Softmax: over z the errors of exp
   // average to at most 10.5 * 2^-23 (of 1024 terms), and the sum has a depth of
   // at most 37: below 2^-17 of the largest score 1 / z in all. The sum with the
-  // bias: 2^-24 |c|.
+  // bias: 2^-24 |c|. Weights that are not renormalised are divided by this z too:
+  // at most those 10.5 * 2^-23 beside the roundings of the sum.
   const float err0 = scores ? (kSigmoid ? 5.f * 0x1p-24f : 0x1p-17f * inv_z) : 0.f;
   const float err1 = bias ? 0x1p-23f : 0.f;
   auto logits_choose = [&]() {   // -0 and +0 are one value
@@ -880,7 +883,7 @@ cudaError_t launch_gate_backward(const moe_shape& s, const moe_gate_desc& g, con
     constexpr int kV = 16 / sizeof(L);
     // the fewest lanes that hold the slots: 8 against 32 lanes 8192 x 256 f32
     // 3.5 / 6.3 us, one token 2.1 / 3.0. A plain softmax keeps its row in registers
-    // (against reading it twice 32768 x 128 bf16 5.2 / 7.9 us, 32768 x 1024 32 / 44)
+    // (32768 x 128 bf16 4.9 us, 32768 x 1024 29; reading it twice 7.9 and 44)
     if constexpr (!kSig && !kRen) {
       if (E % kV == 0 && k <= 8 && E <= 128) return go(gate_backward_kernel<L, kSig, kRen, 8, kV, 16>, l, d, 8);
       if (E % kV == 0 && k <= 8 && E <= 256) return go(gate_backward_kernel<L, kSig, kRen, 8, kV, 32>, l, d, 8);

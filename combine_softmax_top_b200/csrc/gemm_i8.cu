@@ -31,8 +31,8 @@
 //           keep more loads in flight
 // Measured from a cold start: 8192 x 4096 x 7168 141 us, 3.4 POP/s (kPair, 87 % of
 // the tensor pipe; 173 us at the power cap); gate/up of 32 experts, 2 x 2048 x
-// 7168, with 128 rows 148 us = 6.3 TB/s (kOne), with 8192 rows 205 us (kPair, 5.1
-// TB/s and 2.35 POP/s at once).
+// 7168, with 128 rows 148 us = 6.2 TB/s (kOne; 31.45 of the 32 experts have rows on
+// average), with 8192 rows 205 us (kPair, 5.1 TB/s and 2.35 POP/s at once).
 // Every wait is bounded: on expiry the kernel latches MOE_ERR_TIMEOUT, drains
 // its copies and MMAs, frees tensor memory and exits.
 #include <algorithm>
@@ -656,10 +656,12 @@ cudaError_t launch_form(const GemmI8Args& a, int team, bool wide = false) {
 cudaError_t launch_gemm_i8(const GemmI8Args& a) {
   // A few dense rows without tensor cores: integer dot products keep up with the
   // weights while rows x matrices are few, or the weights are soon read.
-  // Measured against the forms here, weights in L2: 7168 x 2048, one / four /
-  // eight rows 3.1 / 3.8 / 5.8 us against 7.5; 8192 x 8192 6.0 / 8.3 / 14.2
-  // against 14; with up 2048 x 7168 7.2 / 7.9 / 9.2 against 11, 4096 x 7168
-  // 10.4 / 17.8 / 25.9 against 14.7
+  // Measured against the forms here, weights in L2 / from HBM, us: 7168 x 2048, one
+  // row 3.3 / 4.5 against 8.4 / 8.9, eight 5.7 / 6.9 against 8.4 / 9.0; 4096 x 7168,
+  // one 4.4 / 7.6 against 10.7 / 12.3, eight 9.3 / 13.9 against 10.9 / 12.4; 8192 x
+  // 8192, four 9.9 / 14.0 against 15.7 / 17.6, eight 17.1 / 19.2 against 15.4 / 18.0;
+  // with up 2048 x 7168, four 6.4 / 9.0 against 11.2 / 12.4; 4096 x 7168, two 11.7 /
+  // 13.8 against 13.8 / 16.4, four 17.3 / 18.4 against 13.7 / 16.3
   const int64_t mats = a.wu ? 2 : 1, sums = a.d.M * mats, weights = mats * a.d.N * a.d.K;
   if (!a.win.offsets && a.d.M <= kFewRows && a.d.M * a.d.K <= kFewBytes &&
       (sums <= 4 || weights <= (sums <= 8 ? 32 : 16) * (int64_t)(1 << 20)))

@@ -7,8 +7,9 @@
 //
 // The tensor-core form needs 3.6 us for one slab of K (barriers, tensor memory,
 // tensor maps) and 0.24 us for each further one. Here one row of 7168 x 2048
-// takes 3.1 us against 7.5 (with the weights in L2), of 4096 x 7168 4.3 against
-// 10; launch_gemm_i8 says from where on the tensor cores are ahead.
+// takes 4.5 us against 8.9 (3.3 against 8.4 with the weights in L2), of 4096 x 7168
+// 7.6 against 12.3 (4.4 against 10.7), where HBM alone would allow 2.2 and 4.5;
+// launch_gemm_i8 says from where on the tensor cores are ahead.
 #include "gemm_i8.cuh"
 
 namespace moe {
