@@ -583,3 +583,35 @@ assert times[0][1] * 3 < times[0][0], times
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("up", [False, True])
+@pytest.mark.parametrize("M,N,K,windows_of", [(2000, 4100, 160, 0), (1500, 1100, 272, 40), (700, 600, 2064, 150)])
+def test_many_units_captured_and_on_few_sms(M, N, K, windows_of, up, ws):
+    """More units than workers, so that the grid is asked for in the call: in a
+    capture, and on a green context's stream; the same bits as on this one."""
+    E = max(1, M // windows_of) if windows_of else 1
+    x, xs = ints((M, K), 1).cuda(), scales(M, 2, 1 / 64).cuda()
+    w, wsc = ints((E, N, K), 3).cuda(), scales(E * N, 4, 0.05 / K ** 0.5).view(E, N).cuda()
+    kw = dict(w_up=ints((E, N, K), 5).cuda(), up_scale=scales(E * N, 6, 0.05 / K ** 0.5).view(E, N).cuda()) if up else {}
+    if windows_of:
+        off = torch.arange(E, dtype=torch.int32, device="cuda") * windows_of
+        kw.update(offsets=off, counts=torch.full_like(off, windows_of))
+    else:
+        w, wsc = w[0], wsc[0]
+        kw = {n: t[0] for n, t in kw.items()}
+    ys = [torch.zeros(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    moe.moe_gemm_i8(x, xs, w, wsc, ys[0], ws, **kw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_gemm_i8(x, xs, w, wsc, ys[1], ws, **kw)
+    graph.replay()
+    torch.cuda.synchronize()
+    part = moe.GreenPartition(16, torch.cuda.current_device())
+    try:
+        moe.moe_gemm_i8(x, xs, w, wsc, ys[2], ws, stream=torch.cuda.ExternalStream(part.dispatch_stream), **kw)
+        torch.cuda.synchronize()
+    finally:
+        part.close()
+    assert moe.moe_poll_status(ws) == 0
+    assert bool(ys[0].any()) and torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
